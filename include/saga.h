@@ -106,8 +106,9 @@ typedef enum {
     SAGA_ERR_CUDA = -4,         /* a CUDA call or launch failed */
     SAGA_ERR_DEVICE = -5,       /* no device, or the device is not sm_100 */
     SAGA_ERR_TIMEOUT = -6,      /* saga_workspace_error: a bounded device wait ran out */
-    SAGA_ERR_BOUNDS = -7        /* saga_workspace_error, debug builds (SAGA_DEBUG): a kernel read
-                                   a position, count or slot out of range and skipped it */
+    SAGA_ERR_BOUNDS = -7        /* saga_workspace_error: a kernel read a position, count or slot out
+                                   of range and skipped it (the paged calls: a length, page or list
+                                   entry of the caller's; others in debug builds, SAGA_DEBUG, only) */
 } saga_status;
 
 /* Bytes of workspace the calls below need for these dimensions.  Depends on
@@ -284,6 +285,123 @@ int saga_topn_refresh_noalloc(const saga_dims* dims, int32_t N, const float* log
 int saga_cache_append(const saga_dims* dims, const void* k_new, const void* v_new, void* k,
                       void* v, saga_stream_t stream);
 
+/* ---- Paged 4-bit cache (the pages keep a bf16 cache; this is an extension) ----
+ * A key/value cache of many sequences of different lengths, in pages of
+ * page_size positions taken from one pool, every row of a head held as
+ * signed 4-bit numbers with one bf16 scale: 3.8 (d = 64) to 3.9 times (d =
+ * 128) smaller than the bf16 cache above.  Layouts:
+ *   k_pages [n_pages, h_k, block(head_dim)]   uint8
+ *   v_pages [n_pages, h_v, block(v_head_dim)] uint8
+ *     block(d): page_size rows of d/2 bytes (byte c of a row holds dim 2c in
+ *     its low and dim 2c+1 in its high four bits, each as n + 8), then
+ *     page_size bf16 scales; the row stands for n * scale, -7 <= n <= 7.
+ *   bounds  [n_pages, h_k, 2, head_dim] bf16  per dim the smallest, then the
+ *     largest of the page's (rotated, not yet rounded to 4 bits) keys
+ *   page_table [batch, max_pages] int32  pool page of positions
+ *     [p * page_size, (p + 1) * page_size) of the sequence; entries past the
+ *     last page of a sequence are never read
+ *   seq_lens [batch] int32  cached positions, 0 .. max_pages * page_size
+ * Lengths, page table and lists are read on the device, so captured calls
+ * follow them.  Every one that is out of range (a negative length, a page
+ * outside the pool, a list entry past the sequence) is skipped and sets the
+ * sticky flag that saga_workspace_error reports as SAGA_ERR_BOUNDS.  Rows past
+ * a sequence's end and pages outside its table hold anything.
+ * Supported shapes: head_dim = v_head_dim in {64, 128}, or 32 with 64; h_k in
+ * {1, 2, 4, 8}; h_v a multiple of h_k, h_q of h_v, h_q/h_k <= 16, h_q <= 128;
+ * page_size in {16, 32, 64}; batch*h_q <= 65535; max_pages*page_size <= 2^30.
+ * The conventions above (ownership, streams, workspace, validation) hold;
+ * pointers of 32-bit values need 4-byte alignment only. */
+typedef struct {
+    int32_t batch;      /* sequences                                  */
+    int32_t h_q;        /* query heads                                */
+    int32_t h_k;        /* key heads                                  */
+    int32_t h_v;        /* value heads                                */
+    int32_t head_dim;   /* key (and query) head dim                   */
+    int32_t v_head_dim; /* value head dim; 0 means head_dim           */
+    int32_t page_size;  /* positions per page                         */
+    int32_t max_pages;  /* columns of the page table                  */
+    int32_t n_pages;    /* pages in the pool                          */
+} saga_paged_dims;
+
+/* Position rotation: pair (x1, x2) of a row at position p becomes
+ * (x1 c - x2 s, x2 c + x1 s) with c = table[p][i], s = table[p][rot_dim/2 + i]
+ * for pair i < rot_dim/2, computed exactly to one fp32 rounding and stored as
+ * bf16.  Pair i is dims (i, i + rot_dim/2), or (2i, 2i+1) with interleaved;
+ * dims from rot_dim on stay as they are.  rot_dim: a multiple of 16, at most
+ * head_dim. */
+typedef struct {
+    const float* table;  /* [max_pos, rot_dim] fp32: cosines, then sines */
+    int32_t max_pos;
+    int32_t rot_dim;
+    int32_t interleaved;
+} saga_rope;
+
+/* Bytes of workspace of the paged calls (0 for unsupported dims); zeroed once
+ * by the caller, as above. */
+size_t saga_paged_workspace_bytes(const saga_paged_dims* dims);
+
+/* Appends n_tokens new rows: sequence b gets rows cu_new[b] .. cu_new[b+1]-1
+ * (cu_new [batch+1], cu_new[0] = 0, cu_new[batch] = n_tokens; null: one row each, n_tokens = batch) at
+ * positions seq_lens[b] ...  Keys (and queries) are rotated first (rope null:
+ * not); each row of a head is then held as
+ *   scale = bf16(max|x| / 7), n = clamp(round-half-even(x / scale), -7, 7)
+ * (n = 0 where the scale is 0).
+ *   k_new [n_tokens, h_k, head_dim], v_new [n_tokens, h_v, v_head_dim], q_new
+ *   [n_tokens, h_q, head_dim] bf16, rows k_stride, v_stride, q_stride elements
+ *   apart (multiples of 8; slices of a fused projection's output will do).
+ *   q_out [n_tokens, h_q, head_dim] bf16: the rotated queries; q_new and
+ *   q_out null: keys and values only.
+ *   bounds (nullable): the touched pages' key bounds, set anew where the call
+ *   writes a page's first row, else widened.
+ *   lens_out (nullable): the grown lengths; may be seq_lens itself.
+ * A page that the call writes to belongs to one sequence only.  Rows past
+ * max_pages * page_size or whose position is not in the rotation table are
+ * not written (nor their queries) and set the sticky flag; so is the whole
+ * page's part of the run where one of its positions is past the table. */
+int saga_paged_append(const saga_paged_dims* dims, int32_t n_tokens, const int32_t* cu_new,
+                      const int32_t* seq_lens, const int32_t* page_table, const void* k_new,
+                      int64_t k_stride, const void* v_new, int64_t v_stride, const void* q_new,
+                      int64_t q_stride, const saga_rope* rope, void* k_pages, void* v_pages,
+                      void* bounds, void* q_out, int32_t* lens_out, void* ws, size_t ws_bytes,
+                      saga_stream_t stream);
+
+/* The way back: rows start[b] .. of each sequence (as many as cu gives it, as
+ * in saga_paged_append) as bf16(n * scale):
+ *   k_out [n_tokens, h_k, head_dim], v_out [n_tokens, h_v, v_head_dim].
+ * With start = 0 and one sequence this is the contiguous cache that the calls
+ * above read. */
+int saga_paged_read(const saga_paged_dims* dims, int32_t n_tokens, const int32_t* cu,
+                    const int32_t* start, const int32_t* page_table, const void* k_pages,
+                    const void* v_pages, void* k_out, void* v_out, void* ws, size_t ws_bytes,
+                    saga_stream_t stream);
+
+/* Picks the pages that each key head's queries attend to: at most n_sel of the
+ * sequence's pages, always its first n_first and last n_last (n_first + n_last
+ * <= n_sel), the rest by descending score, of equal ones the lower index:
+ *   score(page) = max over the key head's query heads of
+ *                 sum_d max(q_d * bounds[page,0,d], q_d * bounds[page,1,d]),
+ * compared in 64 bits: no key of the page has a larger q.k.
+ *   q [batch, h_q, head_dim] bf16 (rotated)
+ *   sel_pages [batch, h_k, n_sel] int32: page indices in the sequence,
+ *   ascending; entries past sel_cnt are left as they were.
+ *   sel_cnt [batch, h_k] int32: min(n_sel, the sequence's pages). */
+int saga_paged_select(const saga_paged_dims* dims, int32_t n_sel, int32_t n_first, int32_t n_last,
+                      const void* q, const void* bounds, const int32_t* seq_lens,
+                      const int32_t* page_table, int32_t* sel_pages, int32_t* sel_cnt, void* ws,
+                      size_t ws_bytes, saga_stream_t stream);
+
+/* One query token per sequence over the paged cache:
+ *   out[b,i,:] = softmax_j(q[b,i].k[b,j,kh(i)] / sqrt(head_dim)) v[b,j,vh(i),:]
+ * over all positions j < seq_lens[b] (sel_pages null), or those of the pages
+ * sel_pages[b, kh(i), 0 .. sel_cnt[b, kh(i)] - 1] (each listed once, in any
+ * order).  out [batch, h_q, v_head_dim] fp32; rows of zeros where there is no
+ * position.  The numbers are multiplied as they are (exact in fp16), scales are
+ * applied to logits and probabilities in fp32. */
+int saga_paged_decode(const saga_paged_dims* dims, const void* q, const void* k_pages,
+                      const void* v_pages, const int32_t* seq_lens, const int32_t* page_table,
+                      const int32_t* sel_pages, const int32_t* sel_cnt, int32_t n_sel, float* out,
+                      void* ws, size_t ws_bytes, saga_stream_t stream);
+
 /* Failure-path self-test (the paper has no counterpart): one CTA waits, with
  * the bounded wait every pipelined kernel uses, on a barrier that nothing
  * completes; after limit_us microseconds (1 .. 1000000) it gives up, sets the
@@ -296,7 +414,8 @@ int saga_selftest_wait_timeout(void* ws, size_t ws_bytes, uint32_t limit_us, sag
 int saga_workspace_reset(void* ws, size_t ws_bytes, saga_stream_t stream);
 
 /* Synchronise `stream`, read and clear the workspace's sticky device flag:
- * SAGA_OK, SAGA_ERR_TIMEOUT, SAGA_ERR_BOUNDS (debug builds only: the
+ * SAGA_OK, SAGA_ERR_TIMEOUT, SAGA_ERR_BOUNDS (the paged calls: a length,
+ * page or list entry out of range, skipped; otherwise debug builds only: the
  * library compiled with SAGA_DEBUG checks every position, count and slot a
  * kernel takes from another kernel's output, and skips the access instead
  * of trapping), or SAGA_ERR_CUDA if the read itself failed. */

@@ -34,7 +34,8 @@ EXPORTS = (
     "saga_set_kernel_events", "saga_version", "saga_topn_refresh_noalloc",
     "saga_selftest_wait_timeout", "saga_cache_append", "saga_qk_logits", "saga_topn_histogram",
     "saga_topn_select_digit", "saga_atopn_decode_partial", "saga_merge_partials",
-    "saga_atopn_refresh_step", "saga_workspace_empty_rows",
+    "saga_atopn_refresh_step", "saga_workspace_empty_rows", "saga_paged_workspace_bytes",
+    "saga_paged_append", "saga_paged_read", "saga_paged_select", "saga_paged_decode",
 )
 
 
@@ -42,6 +43,16 @@ class SagaDims(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("h_q", ctypes.c_int32), ("h_k", ctypes.c_int32),
                 ("h_v", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("l_kv", ctypes.c_int32),
                 ("l_cap", ctypes.c_int32), ("v_head_dim", ctypes.c_int32)]
+
+
+class SagaPagedDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "h_q", "h_k", "h_v", "head_dim", "v_head_dim",
+                                              "page_size", "max_pages", "n_pages")]
+
+
+class SagaRope(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("max_pos", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
 
 
 class SagaError(RuntimeError):
@@ -93,6 +104,15 @@ def load(path: str | None = None):
         lib.saga_topn_select_digit.argtypes = [D, I32, I32, P, P, P, P]
         lib.saga_atopn_decode_partial.argtypes = [D, P, P, P, P, P, P, P, SZ, P]
         lib.saga_merge_partials.argtypes = [D, P, I32, P, P, P]
+        PD, R, I64 = ctypes.POINTER(SagaPagedDims), ctypes.POINTER(SagaRope), ctypes.c_int64
+        lib.saga_paged_workspace_bytes.argtypes = [PD]
+        lib.saga_paged_workspace_bytes.restype = SZ
+        lib.saga_paged_append.argtypes = [PD, I32, P, P, P, P, I64, P, I64, P, I64, R, P, P, P, P, P, P, SZ, P]
+        lib.saga_paged_read.argtypes = [PD, I32, P, P, P, P, P, P, P, P, SZ, P]
+        lib.saga_paged_select.argtypes = [PD, I32, I32, I32, P, P, P, P, P, P, P, SZ, P]
+        lib.saga_paged_decode.argtypes = [PD, P, P, P, P, P, P, P, I32, P, P, SZ, P]
+        for f in ("saga_paged_append", "saga_paged_read", "saga_paged_select", "saga_paged_decode"):
+            getattr(lib, f).restype = ctypes.c_int
         for f in ("saga_decode_dense", "saga_topn_refresh", "saga_atopn_decode", "saga_atopn_refresh_step",
                   "saga_workspace_reset", "saga_workspace_error", "saga_version", "saga_qk_logits",
                   "saga_topn_histogram", "saga_topn_select_digit", "saga_atopn_decode_partial",
@@ -211,6 +231,48 @@ def merge_partials(d, parts, R: int, out, sel_cnt=None, stream=None) -> None:
     _check("saga_merge_partials",
            load().saga_merge_partials(ctypes.byref(d), _ptr(parts), int(R), _ptr(out),
                                       _ptr(sel_cnt), _stream(stream)))
+
+
+# ---- the paged 4-bit cache
+
+def paged_dims(batch, h_q, h_k, h_v, head_dim, page_size, max_pages, n_pages, v_head_dim=None) -> SagaPagedDims:
+    return SagaPagedDims(batch, h_q, h_k, h_v, head_dim, 0 if v_head_dim is None else v_head_dim, page_size,
+                         max_pages, n_pages)
+
+
+def paged_workspace_bytes(d: SagaPagedDims) -> int:
+    return int(load().saga_paged_workspace_bytes(ctypes.byref(d)))
+
+
+def paged_append(d, n_tokens: int, cu_new, seq_lens, page_table, k_new, v_new, q_new, rope, k_pages, v_pages,
+                 bounds, q_out, lens_out, ws, stream=None) -> None:
+    """rope: a SagaRope, or None.  Rows are stride(0) elements apart."""
+    _check("saga_paged_append", load().saga_paged_append(
+        ctypes.byref(d), int(n_tokens), _ptr(cu_new), _ptr(seq_lens), _ptr(page_table), _ptr(k_new),
+        k_new.stride(0), _ptr(v_new), v_new.stride(0), _ptr(q_new), 0 if q_new is None else q_new.stride(0),
+        None if rope is None else ctypes.byref(rope), _ptr(k_pages), _ptr(v_pages), _ptr(bounds), _ptr(q_out),
+        _ptr(lens_out), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def paged_read(d, n_tokens: int, cu, start, page_table, k_pages, v_pages, k_out, v_out, ws, stream=None) -> None:
+    _check("saga_paged_read", load().saga_paged_read(
+        ctypes.byref(d), int(n_tokens), _ptr(cu), _ptr(start), _ptr(page_table), _ptr(k_pages), _ptr(v_pages),
+        _ptr(k_out), _ptr(v_out), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def paged_select(d, n_sel: int, n_first: int, n_last: int, q, bounds, seq_lens, page_table, sel_pages, sel_cnt, ws,
+                 stream=None) -> None:
+    _check("saga_paged_select", load().saga_paged_select(
+        ctypes.byref(d), int(n_sel), int(n_first), int(n_last), _ptr(q), _ptr(bounds), _ptr(seq_lens),
+        _ptr(page_table), _ptr(sel_pages), _ptr(sel_cnt), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def paged_decode(d, q, k_pages, v_pages, seq_lens, page_table, sel_pages, sel_cnt, n_sel: int, out, ws,
+                 stream=None) -> None:
+    """sel_pages, sel_cnt: the lists of paged_select, or None for every page."""
+    _check("saga_paged_decode", load().saga_paged_decode(
+        ctypes.byref(d), _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(seq_lens), _ptr(page_table), _ptr(sel_pages),
+        _ptr(sel_cnt), int(n_sel), _ptr(out), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
 
 
 def selftest_wait_timeout(ws, limit_us: int, stream=None) -> None:

@@ -300,6 +300,13 @@ int run_logits(const Geometry& g, const DeviceInfo& dev, const void* q, const vo
 
 namespace saga {
 void note_launches(int n) { g_launches += static_cast<uint64_t>(n); }
+int require_device(int* sms) {
+    DeviceInfo dev;
+    const int st = device_info(&dev);
+    *sms = dev.sms;
+    return st;
+}
+void kernel_event(bool stop, cudaStream_t stream) { stop ? ev_stop(stream) : ev_start(stream); }
 
 namespace {
 // The largest dynamic shared-memory limit set so far for each kernel, per device.
@@ -863,7 +870,7 @@ const char* saga_status_string(int status) {
         case SAGA_ERR_CUDA: return "CUDA error";
         case SAGA_ERR_DEVICE: return "no sm_100 device";
         case SAGA_ERR_TIMEOUT: return "a bounded device wait timed out";
-        case SAGA_ERR_BOUNDS: return "an index out of range (debug build check)";
+        case SAGA_ERR_BOUNDS: return "an index out of range";
         default: return "unknown status";
     }
 }

@@ -96,6 +96,11 @@ int radix_chunks(long long rows, int l, int sms);
 SAGA_HD int radix_chunk_len(int l, int chunks) { return ((l + chunks - 1) / chunks + 3) & ~3; }
 // Adds n to the library's launch counter (saga_launch_count).
 void note_launches(int n);
+// The current device's SM count, or a saga_status if it is not an sm_100 one.
+int require_device(int* sms);
+// Records the calling thread's measurement event (saga_set_kernel_events) at
+// the start or end of a call's dominant kernel.
+void kernel_event(bool stop, cudaStream_t stream);
 cudaError_t launch_fill(float* p, long long n, float value, cudaStream_t stream);
 
 // Compare + ordered compaction of one logits row per CTA.

@@ -1,0 +1,213 @@
+"""Host-side driver of the paged 4-bit cache over the C ABI.
+
+``PagedCache`` owns the caller-side state of one layer: the pages, the page
+table, the sequences' lengths (all on the device), the pages' key bounds and
+the workspace.  ``append`` takes a step's or a prompt's new rows in, ``decode``
+attends over every cached position, ``select`` picks the pages a sparse
+``decode`` attends to, ``read`` gives rows back as bf16, and ``step`` is one
+token of every sequence through append, select and decode.  Handing pages to
+sequences (filling ``page_table``) is the caller's, ``grow_table`` a helper for
+the plain case.  All compute runs in libsaga.so; calls only enqueue work on the
+current (or given) stream and follow lengths, table and lists on the device, so
+they can be captured in a CUDA graph (after one uncaptured call of each).
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _lib
+
+
+def block_bytes(page_size: int, dim: int) -> int:
+    """Bytes of one head's block of a page: rows of dim/2 bytes, then bf16 scales."""
+    return page_size * (dim // 2 + 2)
+
+
+def _need(name, t, dtype, shape, device, rows=False):
+    """rows: only the dims after the first have to be contiguous (rows a stride apart)."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}, got "
+                         f"{f'{t.dtype} {tuple(t.shape)}' if isinstance(t, torch.Tensor) else type(t).__name__}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    if not t.is_contiguous():
+        ok = rows and (t.shape[0] <= 1 or t.stride(0) >= t[0].numel()) and (t.shape[0] == 0 or t[0].is_contiguous())
+        if not ok or t.stride(0) % 8:
+            raise ValueError(f"{name} must be contiguous" + (" in each row, rows a multiple of 8 elements apart"
+                                                             if rows else ""))
+
+
+class PagedCache:
+    """See the module's text.  ``rope`` is the rotation table [max_pos, rot_dim]
+    fp32 (cosines, then sines); None: keys and queries come rotated.  Buffers
+    that are not given are allocated: pages uninitialised, the table filled
+    with -1, lengths with 0."""
+
+    def __init__(self, batch, h_q, h_k, h_v, head_dim, n_pages, max_pages, page_size=64, v_head_dim=None, rope=None,
+                 rot_dim=None, interleaved=False, k_pages=None, v_pages=None, bounds=None, page_table=None,
+                 seq_lens=None, device="cuda"):
+        self.dv = int(head_dim if v_head_dim is None else v_head_dim)
+        self.dims = _lib.paged_dims(batch, h_q, h_k, h_v, head_dim, page_size, max_pages, n_pages, self.dv)
+        nbytes = _lib.paged_workspace_bytes(self.dims)
+        if nbytes == 0:
+            raise _lib.SagaError("saga_paged_workspace_bytes", _lib.SAGA_ERR_UNSUPPORTED)
+        given = [t for t in (k_pages, v_pages, bounds, page_table, seq_lens, rope) if t is not None]
+        device = given[0].device if given else torch.device(device)
+        if device.type == "cuda" and device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        self.device = device
+
+        def buffer(name, t, dtype, shape, fill=None):
+            if t is None:
+                return torch.empty(shape, dtype=dtype, device=device) if fill is None else \
+                    torch.full(shape, fill, dtype=dtype, device=device)
+            _need(name, t, dtype, shape, device)
+            return t
+
+        u8, i32 = torch.uint8, torch.int32
+        self.k_pages = buffer("k_pages", k_pages, u8, (n_pages, h_k, block_bytes(page_size, head_dim)))
+        self.v_pages = buffer("v_pages", v_pages, u8, (n_pages, h_v, block_bytes(page_size, self.dv)))
+        self.bounds = buffer("bounds", bounds, torch.bfloat16, (n_pages, h_k, 2, head_dim), 0)
+        self.page_table = buffer("page_table", page_table, i32, (batch, max_pages), -1)
+        self.seq_lens = buffer("seq_lens", seq_lens, i32, (batch,), 0)
+        self.rope, self._rope = rope, None
+        if rope is not None:
+            rot = int(rope.shape[-1] if rot_dim is None else rot_dim)
+            _need("rope", rope, torch.float32, (rope.shape[0], rot), device)
+            self._rope = _lib.SagaRope(rope.data_ptr(), rope.shape[0], rot, int(bool(interleaved)))
+        elif rot_dim:
+            raise ValueError("rot_dim without a rotation table")
+        self.ws = torch.zeros(nbytes, dtype=u8, device=device)
+
+    def _on(self, stream):
+        """The stream to enqueue on: the given one, or the cache's device's current one."""
+        return torch.cuda.current_stream(self.device) if stream is None else stream
+
+    def _call(self, fn, *args, stream):
+        if self.device.type == "cuda" and self.device.index != torch.cuda.current_device():
+            with torch.cuda.device(self.device):
+                fn(*args, self._on(stream))
+        else:
+            fn(*args, self._on(stream))
+
+    def grow_table(self, lens) -> None:
+        """Hands pool pages to sequences in order, enough for lens[b] positions
+        of sequence b each (host numbers); the whole table is written."""
+        d = self.dims
+        need = [-(-int(n) // d.page_size) for n in lens]
+        if len(need) != d.batch or any(n < 0 for n in lens) or max(need) > d.max_pages or sum(need) > d.n_pages:
+            raise ValueError("the pool or the table does not hold these lengths")
+        rows, at = torch.full((d.batch, d.max_pages), -1, dtype=torch.int32), 0
+        for b, n in enumerate(need):
+            rows[b, :n] = torch.arange(at, at + n, dtype=torch.int32)
+            at += n
+        self.page_table.copy_(rows)
+
+    def append(self, k_new, v_new, q_new=None, cu_new=None, q_out=None, lens_out=None, stream=None):
+        """New rows ([T, h_k, d], [T, h_v, d_v], queries [T, h_q, d], bf16) at the
+        ends of the sequences: rows cu_new[b] .. cu_new[b+1]-1 are sequence b's
+        (None: one row each).  Returns the rotated queries (None without
+        q_new).  The grown lengths go to seq_lens, or to lens_out if given
+        (seq_lens then stays)."""
+        d, dev, bf = self.dims, self.device, torch.bfloat16
+        T = k_new.shape[0]
+        _need("k_new", k_new, bf, (T, d.h_k, d.head_dim), dev, rows=True)
+        _need("v_new", v_new, bf, (T, d.h_v, self.dv), dev, rows=True)
+        if cu_new is not None:
+            _need("cu_new", cu_new, torch.int32, (d.batch + 1,), dev)
+        elif T != d.batch:
+            raise ValueError("without cu_new there is one new row per sequence")
+        if q_new is not None:
+            _need("q_new", q_new, bf, (T, d.h_q, d.head_dim), dev, rows=True)
+            if q_out is None:
+                q_out = torch.empty((T, d.h_q, d.head_dim), dtype=bf, device=dev)
+            else:
+                _need("q_out", q_out, bf, (T, d.h_q, d.head_dim), dev)
+        elif q_out is not None:
+            raise ValueError("q_out without q_new")
+        if lens_out is None:
+            lens_out = self.seq_lens
+        else:
+            _need("lens_out", lens_out, torch.int32, (d.batch,), dev)
+        self._call(_lib.paged_append, d, T, cu_new, self.seq_lens, self.page_table, k_new, v_new, q_new, self._rope,
+                   self.k_pages, self.v_pages, self.bounds, q_out, lens_out, self.ws, stream=stream)
+        return q_out
+
+    def read(self, n_tokens, cu=None, start=None, k_out=None, v_out=None, stream=None):
+        """Rows start[b] .. of each sequence (None: from seq_lens, the rows an
+        append with lens_out wrote) as bf16 ([T, h_k, d], [T, h_v, d_v])."""
+        d, dev, bf = self.dims, self.device, torch.bfloat16
+        if cu is not None:
+            _need("cu", cu, torch.int32, (d.batch + 1,), dev)
+        elif n_tokens != d.batch:
+            raise ValueError("without cu one row of each sequence is read")
+        if start is None:
+            start = self.seq_lens
+        else:
+            _need("start", start, torch.int32, (d.batch,), dev)
+        shapes = (n_tokens, d.h_k, d.head_dim), (n_tokens, d.h_v, self.dv)
+        if k_out is None:
+            k_out = torch.empty(shapes[0], dtype=bf, device=dev)
+        else:
+            _need("k_out", k_out, bf, shapes[0], dev)
+        if v_out is None:
+            v_out = torch.empty(shapes[1], dtype=bf, device=dev)
+        else:
+            _need("v_out", v_out, bf, shapes[1], dev)
+        self._call(_lib.paged_read, d, n_tokens, cu, start, self.page_table, self.k_pages, self.v_pages, k_out, v_out,
+                   self.ws, stream=stream)
+        return k_out, v_out
+
+    def select(self, q, n_sel, first=1, last=1, pages_out=None, count_out=None, stream=None):
+        """The pages (at most n_sel, [batch, h_k, n_sel] int32, ascending, and
+        their number [batch, h_k]) that each key head's queries attend to: the
+        first and last ones and those with the largest bounds on their logits."""
+        d, dev, i32 = self.dims, self.device, torch.int32
+        _need("q", q, torch.bfloat16, (d.batch, d.h_q, d.head_dim), dev)
+        if pages_out is None:
+            pages_out = torch.zeros((d.batch, d.h_k, n_sel), dtype=i32, device=dev)
+        else:
+            _need("pages_out", pages_out, i32, (d.batch, d.h_k, n_sel), dev)
+        if count_out is None:
+            count_out = torch.empty((d.batch, d.h_k), dtype=i32, device=dev)
+        else:
+            _need("count_out", count_out, i32, (d.batch, d.h_k), dev)
+        self._call(_lib.paged_select, d, n_sel, first, last, q, self.bounds, self.seq_lens, self.page_table,
+                   pages_out, count_out, self.ws, stream=stream)
+        return pages_out, count_out
+
+    def decode(self, q, pages=None, count=None, out=None, stream=None):
+        """Attention of one query token per sequence ([batch, h_q, d] bf16,
+        rotated) over every cached position, or over select's pages; fp32."""
+        d, dev = self.dims, self.device
+        _need("q", q, torch.bfloat16, (d.batch, d.h_q, d.head_dim), dev)
+        if (pages is None) != (count is None):
+            raise ValueError("pages and count go together")
+        n_sel = 0
+        if pages is not None:
+            n_sel = pages.shape[-1]
+            _need("pages", pages, torch.int32, (d.batch, d.h_k, n_sel), dev)
+            _need("count", count, torch.int32, (d.batch, d.h_k), dev)
+        if out is None:
+            out = torch.empty((d.batch, d.h_q, self.dv), dtype=torch.float32, device=dev)
+        else:
+            _need("out", out, torch.float32, (d.batch, d.h_q, self.dv), dev)
+        self._call(_lib.paged_decode, d, q, self.k_pages, self.v_pages, self.seq_lens, self.page_table, pages, count,
+                   n_sel, out, self.ws, stream=stream)
+        return out
+
+    def step(self, k_new, v_new, q_new, n_sel=None, first=1, last=1, out=None, stream=None):
+        """One token of every sequence: its rows appended, its query attended
+        over the grown cache (over at most n_sel pages per key head if given)."""
+        q = self.append(k_new, v_new, q_new, stream=stream)
+        pages = count = None
+        if n_sel is not None:
+            pages, count = self.select(q, n_sel, first, last, stream=stream)
+        return self.decode(q, pages, count, out, stream=stream)
+
+    def error(self, stream=None) -> int:
+        """The sticky device flag (read and cleared; synchronises the stream)."""
+        if self.device.type == "cuda" and self.device.index != torch.cuda.current_device():
+            with torch.cuda.device(self.device):
+                return _lib.workspace_error(self.ws, self._on(stream))
+        return _lib.workspace_error(self.ws, self._on(stream))
