@@ -9,12 +9,13 @@
 
 namespace saga {
 
-// Grid of the paged decode kernel at most (sizes its partial records).
-constexpr int kPagedMaxCtas = 512;
-// Query heads of one decode work row at most (NVU value heads x their query heads).
-constexpr int kPagedMaxRowHeads = 16;
-// Partial record of one query head: largest logit, sum of exponentials, o[dv].
-constexpr int kPagedRecHeader = 2;
+// Grid of the paged decode kernel at most, and its warps per CTA (they size
+// the partial records).
+constexpr int kPagedMaxCtas = 320;
+constexpr int kPagedWarps = 8;
+// Partial record of one query head: largest logit (in powers of two), sum of
+// exponentials, two words of padding, o[dv].
+constexpr int kPagedRecHeader = 4;
 
 struct PagedGeom {
     int b, hq, hk, hv, dk, dv;
@@ -33,10 +34,26 @@ SAGA_HD int paged_block_bytes(int P, int d) { return P * (d / 2 + 2); }
 struct PagedWsLayout {
     size_t err;      // uint32 sticky flag; word 2: the append's ticket (256-byte header)
     size_t tickets;  // uint32 [b*hv]
-    size_t records;  // float  [kPagedMaxCtas][2][kPagedMaxRowHeads][dv + kPagedRecHeader]
+    size_t records;  // float  [kPagedMaxCtas][2][heads of a work row][dv + kPagedRecHeader]
+    size_t firsts;   // float  [kPagedMaxCtas][kPagedWarps][heads of a work row][dv + kPagedRecHeader]
     size_t scores;   // double [b*hk][max_pages]
     size_t total;
 };
+
+// How the decode kernel cuts a key head's value heads into work rows: NVU of
+// them, whose query heads stand in columns of the tensor-core tiles, CW
+// columns to a value head.
+struct PagedRowShape {
+    int CW, NVU;
+};
+SAGA_HD PagedRowShape paged_row_shape(const PagedGeom& g) {
+    const int CW = g.Gv <= 4 ? 4 : g.Gv <= 8 ? 8 : 16;
+    // four value heads only where their accumulators fit in registers beside two more CTAs' worth
+    const int most = CW == 16 ? 1 : CW == 8 ? 2 : g.dv == 64 ? 4 : 2;
+    int NVU = 1;
+    while (NVU * 2 <= most && g.nvk % (NVU * 2) == 0) NVU *= 2;
+    return PagedRowShape{CW, NVU};
+}
 
 inline PagedWsLayout paged_workspace_layout(const PagedGeom& g) {
     PagedWsLayout w{};
@@ -48,7 +65,9 @@ inline PagedWsLayout paged_workspace_layout(const PagedGeom& g) {
     };
     w.err = take(256);
     w.tickets = take(static_cast<size_t>(g.b) * g.hv * sizeof(uint32_t));
-    w.records = take(static_cast<size_t>(kPagedMaxCtas) * 2 * kPagedMaxRowHeads * (g.dv + kPagedRecHeader) * sizeof(float));
+    const size_t rec = static_cast<size_t>(paged_row_shape(g).NVU) * g.Gv * (g.dv + kPagedRecHeader) * sizeof(float);
+    w.records = take(kPagedMaxCtas * 2 * rec);
+    w.firsts = take(static_cast<size_t>(kPagedMaxCtas) * kPagedWarps * rec);
     w.scores = take(static_cast<size_t>(g.b) * g.hk * g.max_pages * sizeof(double));
     w.total = off;
     return w;
@@ -102,6 +121,7 @@ struct PagedDecodeArgs {
     int n_sel;
     float* out;
     float* records;
+    float* firsts;
     uint32_t* tickets;
     uint32_t* err;
 };

@@ -212,6 +212,7 @@ int saga_paged_decode(const saga_paged_dims* dims, const void* q, const void* k_
     a.n_sel = sel_pages ? n_sel : 0;
     a.out = out;
     a.records = ws_at<float>(ws, L.records);
+    a.firsts = ws_at<float>(ws, L.firsts);
     a.tickets = ws_at<uint32_t>(ws, L.tickets);
     a.err = ws_at<uint32_t>(ws, L.err);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
