@@ -27,7 +27,7 @@ struct PagedGeom {
     int kblk, vblk; // bytes of one head's block: P rows of d/2 bytes, then P bf16 scales
 };
 
-SAGA_HD int paged_block_bytes(int P, int d) { return P * (d / 2 + 2); }
+SAGA_HD constexpr int paged_block_bytes(int P, int d) { return P * (d / 2 + 2); }
 
 // Offsets up to `scores` depend on the batch and head counts only; the
 // tickets are zero on entry and left at zero.
@@ -125,6 +125,9 @@ struct PagedDecodeArgs {
     uint32_t* tickets;
     uint32_t* err;
 };
-cudaError_t launch_paged_decode(const PagedDecodeArgs& a, int sms, cudaStream_t stream);
+// by key head dim (one source file each)
+cudaError_t launch_paged_decode_d32(const PagedDecodeArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_paged_decode_d64(const PagedDecodeArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_paged_decode_d128(const PagedDecodeArgs& a, int sms, cudaStream_t stream);
 
 }  // namespace saga

@@ -217,7 +217,9 @@ int saga_paged_decode(const saga_paged_dims* dims, const void* q, const void* k_
     a.err = ws_at<uint32_t>(ws, L.err);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     kernel_event(false, s);
-    const cudaError_t e = launch_paged_decode(a, sms, s);
+    const cudaError_t e = g.dk == 128  ? launch_paged_decode_d128(a, sms, s)
+                          : g.dk == 64 ? launch_paged_decode_d64(a, sms, s)
+                                       : launch_paged_decode_d32(a, sms, s);
     kernel_event(true, s);
     note_launches(1);
     return finish(e);

@@ -23,8 +23,12 @@
 // range is finished there; the pieces of a row that crosses ranges are merged
 // per CTA in shared memory and across CTAs by the row's last one (a ticket,
 // fixed order: results do not depend on timing).
+#pragma once
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "paged.h"
 #include "saga_device.cuh"
@@ -50,7 +54,17 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
-// D += A(16x16, row) * B(16x8, col), fp16 in, fp32 sums.
+// D = A(16x16, row) * B(16x8, col) + C, fp16 in, fp32 sums.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1, float c0, float c1, float c2, float c3) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+
+// D += A(16x16, row) * B(16x8, col).
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
     asm volatile(
@@ -82,9 +96,15 @@ __device__ __forceinline__ float pow2i(int e) { return __uint_as_float(static_ca
 // (bit 0) or last (bit 1), and the valid positions of each of its pages.
 struct StageMeta {
     int row, flags;
+    int full;  // every position of every page is valid
+    int pad;
     int valid[kMaxEntries];
-    int pad[2];
 };
+
+template <int V>
+using Int = std::integral_constant<int, V>;
+template <bool V>
+using Bool = std::integral_constant<bool, V>;
 
 // A warp's unfinished piece of a row, for the merge.
 struct Piece {
@@ -111,7 +131,9 @@ struct Partition {
     int C;            // CTAs that share them
 };
 
-template <int DK, int DV, int CW, int NVU>
+// P: positions per page (a template parameter: every offset inside a tile is
+// then an immediate).
+template <int DK, int DV, int CW, int NVU, int P>
 __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
     paged_decode_kernel(const PagedDecodeArgs a, const int stages, const int min_tiles) {
     using S = Shape<DK, DV, CW, NVU>;
@@ -128,7 +150,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
     const PagedGeom& g = a.g;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int gq = lane >> 2, tq = lane & 3;
-    const int EPT = kTile / g.P;
+    constexpr int EPT = kTile / P;                                        // pages per tile
+    constexpr int KBLK = paged_block_bytes(P, DK), VBLK = paged_block_bytes(P, DV);
     const int nvg = g.nvk / NVU;
     const int heads = NVU * g.Gv;  // of a work row
     const int rec = g.dv + kPagedRecHeader;
@@ -143,14 +166,14 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
     // ---- the partition of all tiles, from the lengths
     auto seq_len = [&](int b) {
         const int len = a.seq_lens[b];
-        if (len < 0 || len > g.max_pages * g.P) {
+        if (len < 0 || len > g.max_pages * P) {
             if (lane == 0) raise_device_error(a.err, kErrBounds);
-            return len < 0 ? 0 : g.max_pages * g.P;
+            return len < 0 ? 0 : g.max_pages * P;
         }
         return len;
     };
     auto item_entries = [&](int item) {  // pages of the item's rows
-        if (!a.sel) return (seq_len(item) + g.P - 1) / g.P;
+        if (!a.sel) return (seq_len(item) + P - 1) / P;
         const int n = a.sel_cnt[item];
         if (n < 0 || n > a.n_sel) {
             raise_device_error(a.err, kErrBounds);
@@ -200,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
     const int n_my = static_cast<int>(w1 - w0);
 
     uint8_t* my_ring = ring + static_cast<size_t>(warp) * stages * S::stage_bytes;
-    const int k_bytes = EPT * g.kblk;
+    constexpr int k_bytes = EPT * KBLK;
 
     // ---- producer state: where in which row the next tile to load is
     int p_item = 0, p_sub = 0, p_tile = 0, p_tiles = 0, p_entries = 0, p_len = 0, p_b = 0, p_kh = 0, p_vg = 0;
@@ -237,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
         win_page = -1;
         win_phys = -1;
         if (e < p_entries) {
-            const int np = (p_len + g.P - 1) / g.P;
+            const int np = (p_len + P - 1) / P;
             win_page = a.sel ? a.sel[(static_cast<size_t>(p_b) * g.hk + p_kh) * a.n_sel + e] : e;
             if (win_page >= 0 && win_page < np) win_phys = a.page_table[static_cast<size_t>(p_b) * g.max_pages + win_page];
             if (win_phys < 0 || win_phys >= g.n_pages) {
@@ -253,22 +276,25 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
         const int src = e0 - win_lo + lane;
         const int phys = __shfl_sync(kFull, win_phys, src & 31), page = __shfl_sync(kFull, win_page, src & 31);
         const bool mine = lane < EPT && phys >= 0;
-        const uint32_t v_bytes = NVU * g.vblk;
+        constexpr uint32_t v_bytes = NVU * VBLK;
         const int live = __popc(__ballot_sync(kFull, mine));
+        const int valid = mine ? min(P, p_len - page * P) : 0;
+        const bool full = __all_sync(kFull, lane >= EPT || valid == P);
         StageMeta& meta = metas[warp][s];
         if (lane == 0) {
             meta.row = p_item * part.mult + p_sub;
             meta.flags = (p_tile == 0 ? 1 : 0) | (p_tile == p_tiles - 1 ? 2 : 0);
-            mbar_arrive_expect_tx(&bars[warp][s], live * (g.kblk + v_bytes));
+            meta.full = full;
+            mbar_arrive_expect_tx(&bars[warp][s], live * (KBLK + v_bytes));
         }
-        if (lane < EPT) meta.valid[lane] = mine ? min(g.P, p_len - page * g.P) : 0;
+        if (lane < EPT) meta.valid[lane] = valid;
         __syncwarp();
         if (mine) {
             const uint32_t dst = smem_addr(my_ring + static_cast<size_t>(s) * S::stage_bytes);
-            bulk_load(dst + lane * g.kblk, a.k_pages + (static_cast<size_t>(phys) * g.hk + p_kh) * g.kblk, g.kblk,
+            bulk_load(dst + lane * KBLK, a.k_pages + (static_cast<size_t>(phys) * g.hk + p_kh) * KBLK, KBLK,
                       &bars[warp][s]);
             bulk_load(dst + k_bytes + lane * v_bytes,
-                      a.v_pages + (static_cast<size_t>(phys) * g.hv + p_kh * g.nvk + p_vg * NVU) * g.vblk, v_bytes,
+                      a.v_pages + (static_cast<size_t>(phys) * g.hv + p_kh * g.nvk + p_vg * NVU) * VBLK, v_bytes,
                       &bars[warp][s]);
         }
         if (++p_tile == p_tiles) {  // on to the next row that has a tile
@@ -424,16 +450,18 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
         }
     };
 
-    // ---- GRP groups of 16 positions from group g0 of the stage's tile
-    auto consume = [&](const uint8_t* buf, const StageMeta& meta, int g0) {
+    // ---- GRP groups of 16 positions from group g0 of the stage's tile; full: every position of it is valid
+    auto consume = [&](const uint8_t* buf, const StageMeta& meta, auto g0_, auto full_) {
+        constexpr int g0 = decltype(g0_)::value;
+        constexpr bool full = decltype(full_)::value;
         float x[GRP][NT][4];
         float sv[GRP][NT][2];
         uint32_t sv_max = 0;
 #pragma unroll
         for (int gi = 0; gi < GRP; ++gi) {
-            const int p0 = (g0 + gi) * 16, e = p0 / g.P, in = p0 % g.P;  // the group's page and its place in it
-            const int valid = meta.valid[e] - in;
-            const uint8_t* kb = buf + e * g.kblk;
+            const int p0 = (g0 + gi) * 16, e = p0 / P, in = p0 % P;  // the group's page and its place in it
+            const int valid = full ? 16 : meta.valid[e] - in;
+            const uint8_t* kb = buf + e * KBLK;
             const uint8_t* krow = kb + (in + pos_a) * (DK / 2) + tq * (WK * 4);
             uint32_t w[2][WK];
 #pragma unroll
@@ -450,20 +478,21 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
                 }
             }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) x[gi][nt][0] = x[gi][nt][2] = c0[nt][0], x[gi][nt][1] = x[gi][nt][3] = c0[nt][1];
-#pragma unroll
             for (int k = 0; k < KS; ++k) {
                 const uint32_t lo = (k & 1) ? w[0][k / 2] >> 8 : w[0][k / 2], hi = (k & 1) ? w[1][k / 2] >> 8 : w[1][k / 2];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float (&c)[4] = x[gi][nt];
                     mma_f16(x[gi][nt], lo & 0x000f000fu, hi & 0x000f000fu, lo & 0x00f000f0u, hi & 0x00f000f0u,
-                            qf[nt][k][0], qf[nt][k][1]);
+                            qf[nt][k][0], qf[nt][k][1], k ? c[0] : c0[nt][0], k ? c[1] : c0[nt][1],
+                            k ? c[2] : c0[nt][0], k ? c[3] : c0[nt][1]);
+                }
             }
-            const __nv_bfloat16* ks = reinterpret_cast<const __nv_bfloat16*>(kb + g.P * (DK / 2)) + in + pos_a;
-            const uint8_t* vb = buf + k_bytes + e * NVU * g.vblk;
+            const __nv_bfloat16* ks = reinterpret_cast<const __nv_bfloat16*>(kb + P * (DK / 2)) + in + pos_a;
+            const uint8_t* vb = buf + k_bytes + e * NVU * VBLK;
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const bool ok = pos_a + 8 * r < valid;
+                const bool ok = full || pos_a + 8 * r < valid;
                 const float s = __bfloat162float(ks[8 * r]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -474,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
                     }
                     // the value head of this lane's columns
                     const int j = CW == 4 ? min(2 * nt + (tq >> 1), NVU - 1) : CW == 8 ? nt : 0;
-                    const uint16_t raw = reinterpret_cast<const uint16_t*>(vb + j * g.vblk + g.P * (DV / 2))[in + pos_a + 8 * r];
+                    const uint16_t raw = reinterpret_cast<const uint16_t*>(vb + j * VBLK + P * (DV / 2))[in + pos_a + 8 * r];
                     const uint32_t bits = ok ? raw : 0u;
                     sv_max = max(sv_max, bits & 0x7fffu);
                     sv[gi][nt][r] = __uint_as_float(bits << 16);
@@ -529,8 +558,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
             for (int i = 0; i < 2; ++i) base[nt][i] = m[nt][i] == -kInf ? 0.f : m[nt][i];
 #pragma unroll
         for (int gi = 0; gi < GRP; ++gi) {
-            const int p0 = (g0 + gi) * 16, e = p0 / g.P, in = p0 % g.P;
-            const uint8_t* vb = buf + k_bytes + e * NVU * g.vblk;
+            const int p0 = (g0 + gi) * 16, e = p0 / P, in = p0 % P;
+            const uint8_t* vb = buf + k_bytes + e * NVU * VBLK;
             uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -548,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
                     lo[nt][r] = half2_bits(__floats2half2_rn(y0 - back.x, y1 - back.y));
                 }
             // probabilities with positions along the contraction: per value head (CW 4: both halves in one tile)
-            uint32_t ph[ACC][2], pl[ACC][2];
+            [[maybe_unused]] uint32_t ph[ACC][2], pl[ACC][2];
             if constexpr (CW == 4) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -570,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
 #pragma unroll
                 for (int half = 0; half < DV / 64; ++half) {
                     // word gq (+ 8) of rows tq, tq + 4, tq + 8, tq + 12
-                    const uint32_t* row0 = reinterpret_cast<const uint32_t*>(vb + j * g.vblk + (in + tq) * (DV / 2)) + gq + 8 * half;
+                    const uint32_t* row0 = reinterpret_cast<const uint32_t*>(vb + j * VBLK + (in + tq) * (DV / 2)) + gq + 8 * half;
                     const uint32_t u0 = row0[0], u1 = row0[4 * DV / 8], u2 = row0[8 * DV / 8], u3 = row0[12 * DV / 8];
 #pragma unroll
                     for (int part_ = 0; part_ < 2; ++part_) {  // nibbles 0-3, 4-7 of the words
@@ -623,8 +652,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
         }
         seen |= meta.flags;
         const uint8_t* buf = my_ring + static_cast<size_t>(s) * S::stage_bytes;
-#pragma unroll 1
-        for (int g0 = 0; g0 < 4; g0 += GRP) consume(buf, meta, g0);
+        if (meta.full) {
+            consume(buf, meta, Int<0>{}, Bool<true>{});
+            if constexpr (GRP == 2) consume(buf, meta, Int<2>{}, Bool<true>{});
+        } else {
+            consume(buf, meta, Int<0>{}, Bool<false>{});
+            if constexpr (GRP == 2) consume(buf, meta, Int<2>{}, Bool<false>{});
+        }
         __syncwarp();
         if (produced < n_my) {
             produce(s);
@@ -764,13 +798,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
     }
 }
 
-template <int DK, int DV, int CW, int NVU>
+template <int DK, int DV, int CW, int NVU, int P>
 cudaError_t run(const PagedDecodeArgs& a, int sms, cudaStream_t stream) {
     using S = Shape<DK, DV, CW, NVU>;
     int stages = (S::MINB == 2 ? kHalfRing : kWholeRing) / (kWarps * S::stage_bytes);
     stages = stages > kMaxStages ? kMaxStages : stages;
     const int smem = kWarps * stages * S::stage_bytes;
-    auto kern = paged_decode_kernel<DK, DV, CW, NVU>;
+    auto kern = paged_decode_kernel<DK, DV, CW, NVU, P>;
     const cudaError_t e = allow_dynamic_smem(kern, smem);
     if (e != cudaSuccess) return e;
     int ctas = sms * S::MINB;
@@ -778,23 +812,26 @@ cudaError_t run(const PagedDecodeArgs& a, int sms, cudaStream_t stream) {
     return launch_dependent(kern, dim3(ctas), dim3(kThreads), smem, stream, a, stages, kWarps);
 }
 
+template <int DK, int DV, int CW, int NVU>
+cudaError_t run_page(const PagedDecodeArgs& a, int sms, cudaStream_t stream) {
+    if (a.g.P == 16) return run<DK, DV, CW, NVU, 16>(a, sms, stream);
+    if (a.g.P == 32) return run<DK, DV, CW, NVU, 32>(a, sms, stream);
+    return run<DK, DV, CW, NVU, 64>(a, sms, stream);
+}
+
 template <int DK, int DV>
 cudaError_t run_shape(const PagedDecodeArgs& a, int sms, cudaStream_t stream) {
     const PagedRowShape r = paged_row_shape(a.g);
     if (r.CW == 4) {
-        if (r.NVU == 1) return run<DK, DV, 4, 1>(a, sms, stream);
-        if (r.NVU == 2) return run<DK, DV, 4, 2>(a, sms, stream);
-        if constexpr (DV == 64) return run<DK, DV, 4, 4>(a, sms, stream);
+        if (r.NVU == 1) return run_page<DK, DV, 4, 1>(a, sms, stream);
+        if constexpr (DV == 64)
+            if (r.NVU == 4) return run_page<DK, DV, 4, 4>(a, sms, stream);
+        return run_page<DK, DV, 4, 2>(a, sms, stream);
     }
-    if (r.CW == 8) return r.NVU == 1 ? run<DK, DV, 8, 1>(a, sms, stream) : run<DK, DV, 8, 2>(a, sms, stream);
-    return run<DK, DV, 16, 1>(a, sms, stream);
+    if (r.CW == 8) return r.NVU == 1 ? run_page<DK, DV, 8, 1>(a, sms, stream) : run_page<DK, DV, 8, 2>(a, sms, stream);
+    return run_page<DK, DV, 16, 1>(a, sms, stream);
 }
 
 }  // namespace
-
-cudaError_t launch_paged_decode(const PagedDecodeArgs& a, int sms, cudaStream_t stream) {
-    if (a.g.dk == 128) return run_shape<128, 128>(a, sms, stream);
-    return a.g.dk == 64 ? run_shape<64, 64>(a, sms, stream) : run_shape<32, 64>(a, sms, stream);
-}
 
 }  // namespace saga
