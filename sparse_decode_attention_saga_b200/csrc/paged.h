@@ -9,10 +9,10 @@
 
 namespace saga {
 
-// Grid of the paged decode kernel at most, and its warps per CTA (they size
+// Grid of the paged decode kernel and its warps per CTA at most (they size
 // the partial records).
-constexpr int kPagedMaxCtas = 320;
-constexpr int kPagedWarps = 8;
+constexpr int kPagedMaxCtas = 160;
+constexpr int kPagedWarps = 16;
 // Partial record of one query head: largest logit (in powers of two), sum of
 // exponentials, two words of padding, o[dv].
 constexpr int kPagedRecHeader = 4;
@@ -48,7 +48,7 @@ struct PagedRowShape {
 };
 SAGA_HD PagedRowShape paged_row_shape(const PagedGeom& g) {
     const int CW = g.Gv <= 4 ? 4 : g.Gv <= 8 ? 8 : 16;
-    // four value heads only where their accumulators fit in registers beside two more CTAs' worth
+    // four value heads only where their accumulators fit in registers
     const int most = CW == 16 ? 1 : CW == 8 ? 2 : g.dv == 64 ? 4 : 2;
     int NVU = 1;
     while (NVU * 2 <= most && g.nvk % (NVU * 2) == 0) NVU *= 2;

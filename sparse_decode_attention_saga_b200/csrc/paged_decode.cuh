@@ -19,16 +19,18 @@
 // device from the lengths, are cut into equal contiguous ranges, one per
 // warp, whatever the rows' lengths: a warp runs through its tiles with its
 // own ring of bulk copies (one for the key block and one for the value blocks
-// of a page), no barrier between warps.  A row that ends inside a warp's
-// range is finished there; the pieces of a row that crosses ranges are merged
-// per CTA in shared memory and across CTAs by the row's last one (a ticket,
-// fixed order: results do not depend on timing).
+// of a page).  A row that ends inside a warp's range is finished there; the
+// pieces of a row that crosses ranges are merged per CTA in shared memory and
+// across CTAs by the row's last one (a ticket, fixed order: results do not
+// depend on timing).  One CTA has an SM to itself, and its warps keep within
+// a round of two tiles of one another (a barrier that a warp arrives at after
+// a round and waits for a round later): with two CTAs and no such pace the
+// SM's older warps ran first and left the younger ones to finish alone, at
+// half the issue rate (batch 16 x 128K: CTAs ended at 150 and at 215 us).
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-
-#include <type_traits>
 
 #include "paged.h"
 #include "saga_device.cuh"
@@ -37,16 +39,22 @@ namespace saga {
 
 namespace {
 
-constexpr int kWarps = kPagedWarps;
-constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 64;  // positions per tile
 constexpr int kMaxEntries = kTile / 16;
 constexpr int kMaxStages = 4;
 constexpr uint32_t kFull = 0xffffffffu;
-// Shared memory for a CTA's rings when two CTAs share an SM, and when one has
-// it (228 KB an SM; the static part is below 8 KB a CTA).
-constexpr int kHalfRing = 104 * 1024, kWholeRing = 216 * 1024;
-constexpr float kLog2e = 1.4426950408889634f;
+// Shared memory for a CTA's rings (227 KB at most; the static part is below 10 KB).
+constexpr int kRingBytes = 216 * 1024;
+constexpr int kRound = 2;  // tiles between two arrivals at the pace barrier
+// A probability times its row's scale stands in fp16 in units of 2^-kUnit of the
+// largest scale: room for a logit to pass the accumulators' reference before a
+// new one is taken, when a product reaches 2^15.
+constexpr int kUnit = 8;
+// The reference before a row's first position: its product overflows and brings one.
+constexpr float kNone = -1e30f;
+// log2(e) / sqrt(d): logits count in powers of two
+template <int D>
+constexpr float kLogitScaleOf = D == 32 ? 0.25503486f : D == 64 ? 0.18033688f : 0.12751743f;
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -86,30 +94,33 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return r;
 }
 
+// (x & MASK) | magic in one instruction.
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t magic) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "n"(MASK), "r"(magic));
+    return r;
+}
+
 __device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 __device__ __forceinline__ __half2 bits_half2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
 
 // 2^e for e in [-126, 127].
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
-// What a ring stage holds: its work row, whether the tile is the row's first
-// (bit 0) or last (bit 1), and the valid positions of each of its pages.
+// What a ring stage holds: its work row, which of the row's tiles it is, and
+// the valid positions of each of its pages (a byte each).
 struct StageMeta {
-    int row, flags;
-    int full;  // every position of every page is valid
-    int pad;
-    int valid[kMaxEntries];
+    int row, tile, tiles;
+    uint32_t valid;
 };
-
-template <int V>
-using Int = std::integral_constant<int, V>;
-template <bool V>
-using Bool = std::integral_constant<bool, V>;
 
 // A warp's unfinished piece of a row, for the merge.
 struct Piece {
-    int row;    // -1: none
-    int flags;  // bit 0: holds the row's first tile, bit 1: its last
+    int row;          // -1: none
+    int flags;        // bit 0: holds the row's first tile, bit 1: its last
+    int tiles;        // of the whole row
+    long long tile0;  // the row's first tile among all
 };
 
 template <int DK, int DV, int CW, int NVU>
@@ -119,10 +130,12 @@ struct Shape {
     static constexpr int WK = DK / 32;                                       // words of a key row per lane
     static constexpr int MT = DV / 16;                                       // tiles of 16 value dims
     static constexpr int ACC = CW == 16 ? 2 : NVU;                           // accumulators of MT tiles
-    static constexpr int GRP = NT == 1 ? 4 : 2;  // groups of 16 positions between softmax updates
     static constexpr int stage_bytes = kTile * (DK / 2 + 2) + NVU * kTile * (DV / 2 + 2);
-    // CTAs per SM: two where 128 registers a thread and half the shared memory (two stages) do
-    static constexpr int MINB = (NT == 1 && 2 * kWarps * stage_bytes <= kHalfRing) ? 2 : 1;
+    // warps: as many as two stages each leave room for and their registers
+    // (accumulators and queries beside about 90 to 105 others)
+    static constexpr int by_smem = kRingBytes / (2 * stage_bytes), regs = ACC * MT * 4 + NT * KS * 2 + 72 + 16 * NT;
+    static constexpr int W = by_smem >= 16 && regs <= 128 ? 16 : by_smem >= 12 && regs <= 168 ? 12 : 8;
+    static constexpr int stages = kRingBytes / (W * stage_bytes) < kMaxStages ? kRingBytes / (W * stage_bytes) : kMaxStages;
 };
 
 struct Partition {
@@ -134,17 +147,20 @@ struct Partition {
 // P: positions per page (a template parameter: every offset inside a tile is
 // then an immediate).
 template <int DK, int DV, int CW, int NVU, int P>
-__global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
-    paged_decode_kernel(const PagedDecodeArgs a, const int stages, const int min_tiles) {
+__global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
+    paged_decode_kernel(const PagedDecodeArgs a, const int min_tiles) {
     using S = Shape<DK, DV, CW, NVU>;
-    constexpr int NT = S::NT, KS = S::KS, WK = S::WK, MT = S::MT, ACC = S::ACC, GRP = S::GRP;
+    constexpr int NT = S::NT, KS = S::KS, WK = S::WK, MT = S::MT, ACC = S::ACC;
+    constexpr float kLogitScale = kLogitScaleOf<DK>;
+    constexpr int kWarps = S::W, kThreads = kWarps * 32, stages = S::stages;
     extern __shared__ __align__(16) uint8_t ring[];  // [kWarps][stages][stage bytes]
-    __shared__ uint64_t bars[kWarps][kMaxStages];
-    __shared__ StageMeta metas[kWarps][kMaxStages];
+    __shared__ uint64_t bars[kWarps][stages], pace;
+    __shared__ __align__(16) StageMeta metas[kWarps][stages];
     __shared__ long long prefix[kThreads + 1];
     __shared__ long long warp_sums[kWarps];
     __shared__ Piece pieces[2 * kWarps];
-    __shared__ int group_begin[2 * kWarps + 1], n_groups, group_last[2 * kWarps];
+    __shared__ int piece_list[2 * kWarps], group_begin[2 * kWarps + 1], group_flags[2 * kWarps], n_groups;
+    __shared__ int group_last[2 * kWarps];
     __shared__ int abort_flag;
 
     const PagedGeom& g = a.g;
@@ -157,6 +173,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
     const int rec = g.dv + kPagedRecHeader;
 
     if (lane < stages) mbar_init(&bars[warp][lane], 1);
+    if (threadIdx.x == 0) mbar_init(&pace, kWarps);
     if (threadIdx.x < 2 * kWarps) pieces[threadIdx.x].row = -1;
     if (threadIdx.x == 0) abort_flag = 0;
     fence_mbar_init();
@@ -224,22 +241,22 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
 
     uint8_t* my_ring = ring + static_cast<size_t>(warp) * stages * S::stage_bytes;
     constexpr int k_bytes = EPT * KBLK;
+    constexpr uint32_t v_bytes = NVU * VBLK;
 
     // ---- producer state: where in which row the next tile to load is
-    int p_item = 0, p_sub = 0, p_tile = 0, p_tiles = 0, p_entries = 0, p_len = 0, p_b = 0, p_kh = 0, p_vg = 0;
-    int win_lo = 0, win_page = -1, win_phys = -1;  // this lane's entry of a window of 32
-    auto enter_row = [&]() {
-        const int r = p_item * part.mult + p_sub;  // = (b * hk + kh) * nvg + vg
-        p_vg = r % nvg;
-        p_kh = r / nvg % g.hk;
-        p_b = r / nvg / g.hk;
-        p_len = seq_len(p_b);
-        win_lo = -32;
-    };
+    int p_item = 0, p_sub = 0, p_tile = 0, p_tiles = 0, p_entries = 0;
+    // a window of 32 pages of the row: this lane's page, loaded once for all
+    // the window's tiles and copied by this lane when its tile is due
+    int win_left = 0;  // tiles left in the window
+    const uint8_t *win_k = nullptr, *win_v = nullptr;
+    bool win_live = false;
+    uint32_t win_valid = 0;  // valid positions of the pages of this lane's tile, a byte each
+    const uint32_t lane_dst = smem_addr(my_ring) + (lane % EPT) * KBLK, lane_vdst = smem_addr(my_ring) + k_bytes + (lane % EPT) * v_bytes;
     if (n_my > 0) {
         int c = 0;  // the chunk of items that holds tile w0: the last with prefix <= w0 (never an empty one)
-        for (int step = kThreads / 2; step > 0; step >>= 1)
-            if (prefix[c + step] <= w0) c += step;
+#pragma unroll
+        for (int step = 256; step > 0; step >>= 1)
+            if (c + step < kThreads && prefix[c + step] <= w0) c += step;
         long long at = prefix[c];
         p_item = c * chunk;
         while (true) {
@@ -250,55 +267,61 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
             at += n;
             ++p_item;
         }
-        p_sub = static_cast<int>((w0 - at) / p_tiles);
-        p_tile = static_cast<int>((w0 - at) % p_tiles);
-        enter_row();
+        const unsigned rest = static_cast<unsigned>(w0 - at);  // below tiles x rows of one sequence
+        p_sub = static_cast<int>(rest / p_tiles);
+        p_tile = static_cast<int>(rest % p_tiles);
     }
     auto load_window = [&]() {
+        const int r = p_item * part.mult + p_sub;  // = (b * hk + kh) * nvg + vg
+        const int vg = r % nvg, bk = r / nvg, kh = bk % g.hk, b = bk / g.hk;
+        const int len = seq_len(b);
         const int e = p_tile * EPT + lane;
-        win_lo = p_tile * EPT;
-        win_page = -1;
-        win_phys = -1;
+        win_left = 32 / EPT;
+        win_live = false;
+        uint32_t valid = 0;
         if (e < p_entries) {
-            const int np = (p_len + P - 1) / P;
-            win_page = a.sel ? a.sel[(static_cast<size_t>(p_b) * g.hk + p_kh) * a.n_sel + e] : e;
-            if (win_page >= 0 && win_page < np) win_phys = a.page_table[static_cast<size_t>(p_b) * g.max_pages + win_page];
-            if (win_phys < 0 || win_phys >= g.n_pages) {
+            const int np = (len + P - 1) / P;
+            const int page = a.sel ? a.sel[static_cast<size_t>(bk) * a.n_sel + e] : e;
+            const int phys = page >= 0 && page < np ? a.page_table[static_cast<size_t>(b) * g.max_pages + page] : -1;
+            win_live = phys >= 0 && phys < g.n_pages;
+            if (win_live) {
+                win_k = a.k_pages + (static_cast<size_t>(phys) * g.hk + kh) * KBLK;
+                win_v = a.v_pages + (static_cast<size_t>(phys) * g.hv + kh * g.nvk + vg * NVU) * VBLK;
+                valid = min(P, len - page * P);
+            } else {
                 raise_device_error(a.err, kErrBounds);
-                win_phys = -1;
             }
         }
+        win_valid = valid << (8 * (lane % EPT));
+#pragma unroll
+        for (int o = 1; o < EPT; o <<= 1) win_valid |= __shfl_xor_sync(kFull, win_valid, o);
     };
     // loads the next tile into stage s
     auto produce = [&](int s) {
-        const int e0 = p_tile * EPT;
-        if (e0 < win_lo || e0 - win_lo >= 32) load_window();
-        const int src = e0 - win_lo + lane;
-        const int phys = __shfl_sync(kFull, win_phys, src & 31), page = __shfl_sync(kFull, win_page, src & 31);
-        const bool mine = lane < EPT && phys >= 0;
-        constexpr uint32_t v_bytes = NVU * VBLK;
-        const int live = __popc(__ballot_sync(kFull, mine));
-        const int valid = mine ? min(P, p_len - page * P) : 0;
-        const bool full = __all_sync(kFull, lane >= EPT || valid == P);
-        StageMeta& meta = metas[warp][s];
-        if (lane == 0) {
-            meta.row = p_item * part.mult + p_sub;
-            meta.flags = (p_tile == 0 ? 1 : 0) | (p_tile == p_tiles - 1 ? 2 : 0);
-            meta.full = full;
-            mbar_arrive_expect_tx(&bars[warp][s], live * (KBLK + v_bytes));
+        if (win_left == 0) load_window();
+        const int first = 32 - win_left * EPT;  // the lane of the tile's first page
+        if (lane >= first && lane < first + EPT) {
+            uint64_t* bar = &bars[warp][s];
+            if (EPT > 1) {
+                if (win_live) mbar_expect_tx(bar, KBLK + v_bytes);
+                __syncwarp(((1u << EPT) - 1u) << first);
+            }
+            if (lane == first) {
+                *reinterpret_cast<int4*>(&metas[warp][s]) =
+                    make_int4(p_item * part.mult + p_sub, p_tile, p_tiles, static_cast<int>(win_valid));
+                if (EPT == 1) mbar_arrive_expect_tx(bar, win_live ? KBLK + v_bytes : 0u);
+                else mbar_arrive(bar);
+            }
+            if (win_live) {
+                bulk_load(lane_dst + s * S::stage_bytes, win_k, KBLK, bar);
+                bulk_load(lane_vdst + s * S::stage_bytes, win_v, v_bytes, bar);
+            }
         }
-        if (lane < EPT) meta.valid[lane] = valid;
         __syncwarp();
-        if (mine) {
-            const uint32_t dst = smem_addr(my_ring + static_cast<size_t>(s) * S::stage_bytes);
-            bulk_load(dst + lane * KBLK, a.k_pages + (static_cast<size_t>(phys) * g.hk + p_kh) * KBLK, KBLK,
-                      &bars[warp][s]);
-            bulk_load(dst + k_bytes + lane * v_bytes,
-                      a.v_pages + (static_cast<size_t>(phys) * g.hv + p_kh * g.nvk + p_vg * NVU) * VBLK, v_bytes,
-                      &bars[warp][s]);
-        }
+        --win_left;
         if (++p_tile == p_tiles) {  // on to the next row that has a tile
             p_tile = 0;
+            win_left = 0;
             if (++p_sub == part.mult) {
                 p_sub = 0;
                 do {
@@ -307,7 +330,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
                 } while (p_entries == 0);
                 p_tiles = tiles_of(p_entries);
             }
-            if (p_item < part.items) enter_row();
         }
     };
 
@@ -315,6 +337,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
     int row = -1, seen = 0, expo = 0;  // seen: flags of the row's tiles so far; expo: biased exponent of the largest scale
     uint32_t qf[NT][KS][2];
     float c0[NT][2], colf[NT][2], m[NT][2], l[NT][2];
+    float unit = 0.f;  // factor of the scales, 2^(kUnit - their largest exponent)
     float acc[ACC][MT][4];
     const int pos_a = (gq >> 1) + 4 * (gq & 1);  // position (of 16) of tile row gq; row gq + 8: 8 more
 
@@ -328,6 +351,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
         row = r;
         seen = 0;
         expo = 20;
+        unit = pow2i(kUnit + 127 - 20);
         const int vg = r % nvg, bk = r / nvg;  // bk = b * hk + kh
         const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) +
                                  (static_cast<size_t>(bk) * g.nvk + vg * NVU) * g.Gv * DK;
@@ -347,16 +371,16 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
             big = fmaxf(big, __shfl_xor_sync(kFull, big, 1));
             big = fmaxf(big, __shfl_xor_sync(kFull, big, 2));
             // the head's largest query in [2^14, 2^15): 8 bits of any one down to 2^-27 of it stay whole
-            const int e = big > 0.f ? ilogbf(big) : 0;
-            const int sh = 14 - e;
+            const int sh = min(14 + 127 - static_cast<int>(__float_as_uint(big) >> 23), 126);
+            const float up = pow2i(sh);
             float sum = 0.f;
 #pragma unroll
             for (int w = 0; w < WK; ++w) {
                 float x[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    x[2 * i] = ldexpf(bf16_lo(raw[w][i]), sh);
-                    x[2 * i + 1] = ldexpf(bf16_hi(raw[w][i]), sh);
+                    x[2 * i] = bf16_lo(raw[w][i]) * up;
+                    x[2 * i + 1] = bf16_hi(raw[w][i]) * up;
                 }
                 // pair j holds dims j and j + 4 of the word; odd pairs meet nibbles 16 times their number
 #pragma unroll
@@ -371,12 +395,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
             sum += __shfl_xor_sync(kFull, sum, 1);
             sum += __shfl_xor_sync(kFull, sum, 2);
             const float start = -8.f * sum * 5.9604644775390625e-08f;  // 2^-24: a nibble as an fp16 subnormal
-            const float f = ldexpf(kLog2e * rsqrtf(static_cast<float>(DK)), min(24 - sh, 126));
+            const float f = kLogitScale * pow2i(min(24 - sh, 126));
 #pragma unroll
             for (int i = 0; i < 2; ++i) {  // this lane's columns 2 tq + i
                 c0[nt][i] = __shfl_sync(kFull, start, (2 * tq + i) * 4);
                 colf[nt][i] = __shfl_sync(kFull, f, (2 * tq + i) * 4);
-                m[nt][i] = -kInf;
+                m[nt][i] = kNone;
                 l[nt][i] = 0.f;
             }
         }
@@ -401,27 +425,42 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
         for (int x = 0; x < ACC; ++x) {
             float f[2];
             beside(factor, x, f);
+            if constexpr (CW == 4) {  // columns c and c + 4 are the two halves of one head: the left lanes add
+                                      // them up for dims 8 gq + 2 k, the right ones for 8 gq + 2 k + 1
+                const bool left = tq < 2;
+                const int hl = 2 * (tq & 1);
+                float* at = dst + (x * g.Gv + hl) * stride + 8 * gq + (left ? 0 : 1);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+                for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float v = acc[x][mt][i];
-                    if (CW == 4) v += __shfl_xor_sync(kFull, v, 2);  // the two halves of the probabilities
-                    const int col = CW == 4 ? 2 * (tq & 1) + (i & 1) : 2 * tq + (i & 1);
-                    const int hl = CW == 16 ? 8 * x + col : col;  // head of the value head
-                    const int dim = 8 * (gq + 8 * (mt >> 2)) + 2 * (mt & 3) + (i >> 1);
-                    if (hl < g.Gv && (CW != 4 || tq < 2)) dst[((CW == 16 ? 0 : x) * g.Gv + hl) * stride + dim] = v * f[i & 1];
-                }
+                    for (int i = 0; i < 2; ++i) {
+                        const float mine = left ? acc[x][mt][i] : acc[x][mt][2 + i];
+                        const float other = left ? acc[x][mt][2 + i] : acc[x][mt][i];
+                        const float v = mine + __shfl_xor_sync(kFull, other, 2);
+                        if (hl + i < g.Gv) at[i * stride + 64 * (mt >> 2) + 2 * (mt & 3)] = v * f[i];
+                    }
+            } else {
+                const int hl = (CW == 16 ? 8 * x : 0) + 2 * tq;  // head of the value head
+                float* at = dst + ((CW == 16 ? 0 : x) * g.Gv + hl) * stride + 8 * gq;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (hl + i < g.Gv)
+                            *reinterpret_cast<float2*>(at + i * stride + 64 * (mt >> 2) + 2 * (mt & 3)) =
+                                make_float2(acc[x][mt][i] * f[i], acc[x][mt][2 + i] * f[i]);
+            }
         }
     };
-    auto finish_row = [&](bool end_of_range) {
+    // (the row's number of tiles, and its first among all)
+    auto finish_row = [&](bool end_of_range, int tiles, long long tile0) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) l[nt][i] += __shfl_xor_sync(kFull, l[nt][i], o);
-        const float unit = pow2i(expo - 127 - 13);
+        const float unit = pow2i(expo - 127 - kUnit);
         float f[NT][2];
         if (seen == 3) {
 #pragma unroll
@@ -447,99 +486,126 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
             Piece& p = pieces[2 * warp + (end_of_range ? 1 : 0)];
             p.row = row;
             p.flags = seen;
+            p.tiles = tiles;
+            p.tile0 = tile0;
         }
     };
 
-    // ---- GRP groups of 16 positions from group g0 of the stage's tile; full: every position of it is valid
-    auto consume = [&](const uint8_t* buf, const StageMeta& meta, auto g0_, auto full_) {
-        constexpr int g0 = decltype(g0_)::value;
-        constexpr bool full = decltype(full_)::value;
-        float x[GRP][NT][4];
-        float sv[GRP][NT][2];
-        uint32_t sv_max = 0;
+    // fp16 pairs of 1024, 1032, 1/16 and -72
+    constexpr uint32_t k1024 = 0x64006400u;
+    const __half2 k1032 = bits_half2(0x64086408u), k16th = bits_half2(0x2c002c00u), k72 = bits_half2(0xd480d480u);
+    // the value head of this lane's columns of a tile (CW 4: two value heads to a tile)
+    const int v_lane = CW == 4 ? min(tq >> 1, NVU - 1) * VBLK : 0;
+
+    // ---- 16 positions: group gi of the stage's tile
+    auto consume = [&](const uint8_t* buf, uint32_t tile_valid, uint32_t gi) {
+        const uint32_t e = gi * 16 / P, in = gi * 16 % P;  // the group's page and its place in it
+        const int valid = static_cast<int>((tile_valid >> (8 * e)) & 0xffu) - static_cast<int>(in);
+        const uint8_t* kb = buf + e * KBLK;
+        const uint8_t* krow = kb + (in + pos_a) * (DK / 2) + tq * (WK * 4);
+        const uint8_t* vb = buf + k_bytes + e * NVU * VBLK;
+        uint32_t w[2][WK];
 #pragma unroll
-        for (int gi = 0; gi < GRP; ++gi) {
-            const int p0 = (g0 + gi) * 16, e = p0 / P, in = p0 % P;  // the group's page and its place in it
-            const int valid = full ? 16 : meta.valid[e] - in;
-            const uint8_t* kb = buf + e * KBLK;
-            const uint8_t* krow = kb + (in + pos_a) * (DK / 2) + tq * (WK * 4);
-            uint32_t w[2][WK];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const uint8_t* src = krow + r * 8 * (DK / 2);
-                if constexpr (WK == 1) {
-                    w[r][0] = *reinterpret_cast<const uint32_t*>(src);
-                } else if constexpr (WK == 2) {
-                    const uint2 v = *reinterpret_cast<const uint2*>(src);
-                    w[r][0] = v.x, w[r][1] = v.y;
-                } else {
-                    const uint4 v = *reinterpret_cast<const uint4*>(src);
-                    w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                const uint32_t lo = (k & 1) ? w[0][k / 2] >> 8 : w[0][k / 2], hi = (k & 1) ? w[1][k / 2] >> 8 : w[1][k / 2];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const float (&c)[4] = x[gi][nt];
-                    mma_f16(x[gi][nt], lo & 0x000f000fu, hi & 0x000f000fu, lo & 0x00f000f0u, hi & 0x00f000f0u,
-                            qf[nt][k][0], qf[nt][k][1], k ? c[0] : c0[nt][0], k ? c[1] : c0[nt][1],
-                            k ? c[2] : c0[nt][0], k ? c[3] : c0[nt][1]);
-                }
-            }
-            const __nv_bfloat16* ks = reinterpret_cast<const __nv_bfloat16*>(kb + P * (DK / 2)) + in + pos_a;
-            const uint8_t* vb = buf + k_bytes + e * NVU * VBLK;
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const bool ok = full || pos_a + 8 * r < valid;
-                const float s = __bfloat162float(ks[8 * r]);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float y = x[gi][nt][2 * r + i] * colf[nt][i] * s;
-                        x[gi][nt][2 * r + i] = ok ? y : -kInf;
-                    }
-                    // the value head of this lane's columns
-                    const int j = CW == 4 ? min(2 * nt + (tq >> 1), NVU - 1) : CW == 8 ? nt : 0;
-                    const uint16_t raw = reinterpret_cast<const uint16_t*>(vb + j * VBLK + P * (DV / 2))[in + pos_a + 8 * r];
-                    const uint32_t bits = ok ? raw : 0u;
-                    sv_max = max(sv_max, bits & 0x7fffu);
-                    sv[gi][nt][r] = __uint_as_float(bits << 16);
-                }
+        for (int r = 0; r < 2; ++r) {
+            const uint8_t* src = krow + r * 8 * (DK / 2);
+            if constexpr (WK == 1) {
+                w[r][0] = *reinterpret_cast<const uint32_t*>(src);
+            } else if constexpr (WK == 2) {
+                const uint2 v = *reinterpret_cast<const uint2*>(src);
+                w[r][0] = v.x, w[r][1] = v.y;
+            } else {
+                const uint4 v = *reinterpret_cast<const uint4*>(src);
+                w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
             }
         }
-        // running maxima; accumulators follow when one grows
-        const int top = static_cast<int>(__reduce_max_sync(kFull, sv_max) >> 7);
-        float mn[NT][2];
-        bool grew = top > expo;
+        const uint16_t* ks = reinterpret_cast<const uint16_t*>(kb + P * (DK / 2)) + in + pos_a;
+        uint32_t kscale[2], vscale[NT][2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            kscale[r] = ks[8 * r];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int j = CW == 4 ? 2 * nt : CW == 8 ? nt : 0;
+                vscale[nt][r] = reinterpret_cast<const uint16_t*>(vb + j * VBLK + v_lane + P * (DV / 2))[in + pos_a + 8 * r];
+            }
+        }
+        float x[NT][4];
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+            const uint32_t lo = (k & 1) ? w[0][k / 2] >> 8 : w[0][k / 2], hi = (k & 1) ? w[1][k / 2] >> 8 : w[1][k / 2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float (&c)[4] = x[nt];
+                mma_f16(x[nt], lo & 0x000f000fu, hi & 0x000f000fu, lo & 0x00f000f0u, hi & 0x00f000f0u, qf[nt][k][0],
+                        qf[nt][k][1], k ? c[0] : c0[nt][0], k ? c[1] : c0[nt][1], k ? c[2] : c0[nt][0],
+                        k ? c[3] : c0[nt][1]);
+            }
+        }
+        float off[2] = {0.f, 0.f};  // -inf at the positions past the end, whose scales count as 0
+        if (valid < 16) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                if (pos_a + 8 * r >= valid) {
+                    off[r] = -kInf;
+                    kscale[r] = 0;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) vscale[nt][r] = 0;
+                }
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float v = -kInf;
+            for (int r = 0; r < 2; ++r) {
+                const float s = __uint_as_float(kscale[r] << 16);
 #pragma unroll
-                for (int gi = 0; gi < GRP; ++gi) v = fmaxf(v, fmaxf(x[gi][nt][i], x[gi][nt][2 + i]));
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
-                mn[nt][i] = fmaxf(v, m[nt][i]);
-                grew |= mn[nt][i] > m[nt][i];
+                for (int i = 0; i < 2; ++i) x[nt][2 * r + i] = __fmaf_rn(x[nt][2 * r + i], colf[nt][i] * s, off[r]);
             }
-        if (__any_sync(kFull, grew)) {
-            const int en = max(expo, top);
-            const float shift = en - expo < 126 ? pow2i(expo - en) : 0.f;
-            expo = en;
-            float f[NT][2];
+        // p = 2^(x - reference), y = p times its row's scale, in two fp16 halves
+        float p[NT][4], y[NT][4];
+        uint32_t hi[NT][2], lo[NT][2];
+        auto products = [&]() {
+            __half2 top = bits_half2(0u);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    f[nt][i] = mn[nt][i] == -kInf ? 1.f : exp2_approx(m[nt][i] - mn[nt][i]);
-                    l[nt][i] *= f[nt][i];
-                    m[nt][i] = mn[nt][i];
-                    f[nt][i] *= shift;
+                for (int r = 0; r < 2; ++r) {
+                    const float s = __uint_as_float(vscale[nt][r] << 16) * unit;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        p[nt][2 * r + i] = exp2_approx(x[nt][2 * r + i] - m[nt][i]);
+                        y[nt][2 * r + i] = p[nt][2 * r + i] * s;
+                    }
+                    const __half2 h = __floats2half2_rn(y[nt][2 * r], y[nt][2 * r + 1]);
+                    hi[nt][r] = half2_bits(h);
+                    top = __hmax2_nan(top, h);
                 }
+            return ((half2_bits(top) + 0x08000800u) & 0x80008000u) != 0u;  // a half at 2^15 or above, or no number
+        };
+        if (__any_sync(kFull, products())) {  // a new reference: the largest logit and scale so far
+            uint32_t top = 0;
+            float f[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                top = max(top, max(vscale[nt][0] & 0x7fffu, vscale[nt][1] & 0x7fffu));
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float v = fmaxf(x[nt][i], x[nt][2 + i]);
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+                    v = fmaxf(v, m[nt][i]);
+                    f[nt][i] = exp2_approx(m[nt][i] - v);
+                    l[nt][i] = f[nt][i] > 0.f ? l[nt][i] * f[nt][i] : 0.f;
+                    m[nt][i] = v;
+                }
+            }
+            const int en = max(expo, static_cast<int>(__reduce_max_sync(kFull, top) >> 7));
+            const float shift = en - expo < 126 ? pow2i(expo - en) : 0.f;
+            expo = en;
+            unit = pow2i(kUnit + 127 - en);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) f[nt][i] *= shift;
 #pragma unroll
             for (int xx = 0; xx < ACC; ++xx) {
                 float fx[2];
@@ -549,82 +615,64 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[xx][mt][i] *= fx[i & 1];
             }
+            products();
         }
-        const float unit = pow2i(13 - (expo - 127) < 127 ? 13 - (expo - 127) : 127);
-        float base[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) base[nt][i] = m[nt][i] == -kInf ? 0.f : m[nt][i];
-#pragma unroll
-        for (int gi = 0; gi < GRP; ++gi) {
-            const int p0 = (g0 + gi) * 16, e = p0 / P, in = p0 % P;
-            const uint8_t* vb = buf + k_bytes + e * NVU * VBLK;
-            uint32_t hi[NT][2], lo[NT][2];
+            for (int r = 0; r < 2; ++r) {
+                l[nt][0] += p[nt][2 * r];
+                l[nt][1] += p[nt][2 * r + 1];
+                const float2 back = __half22float2(bits_half2(hi[nt][r]));
+                lo[nt][r] = half2_bits(__floats2half2_rn(y[nt][2 * r] - back.x, y[nt][2 * r + 1] - back.y));
+            }
+        // probabilities with positions along the contraction: per value head (CW 4: both halves in one tile)
+        [[maybe_unused]] uint32_t ph[ACC][2], pl[ACC][2];
+        if constexpr (CW == 4) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const float p0f = exp2_approx(x[gi][nt][2 * r] - base[nt][0]);
-                    const float p1f = exp2_approx(x[gi][nt][2 * r + 1] - base[nt][1]);
-                    l[nt][0] += p0f;
-                    l[nt][1] += p1f;
-                    const float s = sv[gi][nt][r] * unit;
-                    const float y0 = p0f * s, y1 = p1f * s;
-                    const __half2 h = __floats2half2_rn(y0, y1);
-                    const float2 back = __half22float2(h);
-                    hi[nt][r] = half2_bits(h);
-                    lo[nt][r] = half2_bits(__floats2half2_rn(y0 - back.x, y1 - back.y));
+                    const bool left = tq < 2;
+                    const uint32_t got = __shfl_xor_sync(kFull, left ? lo[nt][r] : hi[nt][r], 2);
+                    ph[2 * nt][r] = transpose8x8(left ? hi[nt][r] : got);
+                    if (2 * nt + 1 < NVU) ph[2 * nt + 1 < NVU ? 2 * nt + 1 : 0][r] = transpose8x8(left ? got : lo[nt][r]);
                 }
-            // probabilities with positions along the contraction: per value head (CW 4: both halves in one tile)
-            [[maybe_unused]] uint32_t ph[ACC][2], pl[ACC][2];
-            if constexpr (CW == 4) {
+        } else {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const bool left = tq < 2;
-                        const uint32_t got = __shfl_xor_sync(kFull, left ? lo[nt][r] : hi[nt][r], 2);
-                        ph[2 * nt][r] = transpose8x8(left ? hi[nt][r] : got);
-                        if (2 * nt + 1 < NVU) ph[2 * nt + 1 < NVU ? 2 * nt + 1 : 0][r] = transpose8x8(left ? got : lo[nt][r]);
-                    }
-            } else {
+                for (int r = 0; r < 2; ++r) ph[nt][r] = transpose8x8(hi[nt][r]), pl[nt][r] = transpose8x8(lo[nt][r]);
+        }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+        for (int j = 0; j < NVU; ++j) {
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) ph[nt][r] = transpose8x8(hi[nt][r]), pl[nt][r] = transpose8x8(lo[nt][r]);
-            }
+            for (int half = 0; half < DV / 64; ++half) {
+                // word gq (+ 8) of rows tq, tq + 4, tq + 8, tq + 12
+                const uint32_t* row0 = reinterpret_cast<const uint32_t*>(vb + j * VBLK + (in + tq) * (DV / 2)) + gq + 8 * half;
+                const uint32_t u0 = row0[0], u1 = row0[4 * DV / 8], u2 = row0[8 * DV / 8], u3 = row0[12 * DV / 8];
 #pragma unroll
-            for (int j = 0; j < NVU; ++j) {
+                for (int part_ = 0; part_ < 2; ++part_) {  // nibbles 0-3, 4-7 of the words
+                    const uint32_t sel = part_ ? 0x7632u : 0x5410u;
+                    const uint32_t a_ = __byte_perm(u0, u1, sel), b_ = __byte_perm(u2, u3, sel);
 #pragma unroll
-                for (int half = 0; half < DV / 64; ++half) {
-                    // word gq (+ 8) of rows tq, tq + 4, tq + 8, tq + 12
-                    const uint32_t* row0 = reinterpret_cast<const uint32_t*>(vb + j * VBLK + (in + tq) * (DV / 2)) + gq + 8 * half;
-                    const uint32_t u0 = row0[0], u1 = row0[4 * DV / 8], u2 = row0[8 * DV / 8], u3 = row0[12 * DV / 8];
+                    for (int by = 0; by < 2; ++by) {
+                        const uint32_t av = by ? a_ >> 8 : a_, bv = by ? b_ >> 8 : b_;
+                        const uint32_t f0 = half2_bits(__hsub2(bits_half2(and_or<0x000f000fu>(av, k1024)), k1032));
+                        const uint32_t f1 = half2_bits(__hfma2(bits_half2(and_or<0x00f000f0u>(av, k1024)), k16th, k72));
+                        const uint32_t f2 = half2_bits(__hsub2(bits_half2(and_or<0x000f000fu>(bv, k1024)), k1032));
+                        const uint32_t f3 = half2_bits(__hfma2(bits_half2(and_or<0x00f000f0u>(bv, k1024)), k16th, k72));
+                        const int mt = 4 * half + 2 * part_ + by;
+                        if constexpr (CW == 4) {
+                            mma_f16(acc[j][mt], f0, f1, f2, f3, ph[j][0], ph[j][1]);
+                        } else if constexpr (CW == 8) {
+                            mma_f16(acc[j][mt], f0, f1, f2, f3, ph[j][0], ph[j][1]);
+                            mma_f16(acc[j][mt], f0, f1, f2, f3, pl[j][0], pl[j][1]);
+                        } else {
 #pragma unroll
-                    for (int part_ = 0; part_ < 2; ++part_) {  // nibbles 0-3, 4-7 of the words
-                        const uint32_t sel = part_ ? 0x7632u : 0x5410u;
-                        const uint32_t a_ = __byte_perm(u0, u1, sel), b_ = __byte_perm(u2, u3, sel);
-#pragma unroll
-                        for (int by = 0; by < 2; ++by) {
-                            const uint32_t av = by ? a_ >> 8 : a_, bv = by ? b_ >> 8 : b_;
-                            const __half2 k1032 = __float2half2_rn(1032.f), k16 = __float2half2_rn(0.0625f), k72 = __float2half2_rn(-72.f);
-                            const uint32_t f0 = half2_bits(__hsub2(bits_half2((av & 0x000f000fu) | 0x64006400u), k1032));
-                            const uint32_t f1 = half2_bits(__hfma2(bits_half2((av & 0x00f000f0u) | 0x64006400u), k16, k72));
-                            const uint32_t f2 = half2_bits(__hsub2(bits_half2((bv & 0x000f000fu) | 0x64006400u), k1032));
-                            const uint32_t f3 = half2_bits(__hfma2(bits_half2((bv & 0x00f000f0u) | 0x64006400u), k16, k72));
-                            const int mt = 4 * half + 2 * part_ + by;
-                            if constexpr (CW == 4) {
-                                mma_f16(acc[j][mt], f0, f1, f2, f3, ph[j][0], ph[j][1]);
-                            } else if constexpr (CW == 8) {
-                                mma_f16(acc[j][mt], f0, f1, f2, f3, ph[j][0], ph[j][1]);
-                                mma_f16(acc[j][mt], f0, f1, f2, f3, pl[j][0], pl[j][1]);
-                            } else {
-#pragma unroll
-                                for (int nt = 0; nt < 2; ++nt) {
-                                    mma_f16(acc[nt][mt], f0, f1, f2, f3, ph[nt][0], ph[nt][1]);
-                                    mma_f16(acc[nt][mt], f0, f1, f2, f3, pl[nt][0], pl[nt][1]);
-                                }
+                            for (int nt = 0; nt < 2; ++nt) {
+                                mma_f16(acc[nt][mt], f0, f1, f2, f3, ph[nt][0], ph[nt][1]);
+                                mma_f16(acc[nt][mt], f0, f1, f2, f3, pl[nt][0], pl[nt][1]);
                             }
                         }
                     }
@@ -634,7 +682,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
     };
 
     // ---- the warp's tiles
-    int produced = 0, done = 0;
+    int produced = 0, done = 0, tiles = 0;
+    long long tile0 = 0;
     uint32_t phase = 0;  // bit s: parity to wait for in stage s
     bool ok = true;
     for (; produced < stages && produced < n_my; ++produced) produce(produced);
@@ -644,27 +693,37 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
             break;
         }
         phase ^= 1u << s;
-        const StageMeta& meta = metas[warp][s];
-        const int r = meta.row;
-        if (r != row) {
-            if (row >= 0) finish_row(false);
-            begin_row(r);
+        const int4 meta = *reinterpret_cast<const int4*>(&metas[warp][s]);
+        if (meta.x != row) {
+            if (row >= 0) finish_row(false, tiles, tile0);
+            begin_row(meta.x);
+            tiles = meta.z;
+            tile0 = w0 + done - meta.y;
         }
-        seen |= meta.flags;
-        const uint8_t* buf = my_ring + static_cast<size_t>(s) * S::stage_bytes;
-        if (meta.full) {
-            consume(buf, meta, Int<0>{}, Bool<true>{});
-            if constexpr (GRP == 2) consume(buf, meta, Int<2>{}, Bool<true>{});
-        } else {
-            consume(buf, meta, Int<0>{}, Bool<false>{});
-            if constexpr (GRP == 2) consume(buf, meta, Int<2>{}, Bool<false>{});
-        }
+        seen |= (meta.y == 0 ? 1 : 0) | (meta.y == tiles - 1 ? 2 : 0);
+        const uint8_t* buf = my_ring + s * S::stage_bytes;
+#pragma unroll
+        for (uint32_t gi = 0; gi < kTile / 16; ++gi) consume(buf, meta.w, gi);
         __syncwarp();
         if (produced < n_my) {
             produce(s);
             ++produced;
         }
         s = s + 1 == stages ? 0 : s + 1;
+        if (done % kRound == kRound - 1 && done + 1 < n_my) {  // end of round done / kRound
+            const int round = done / kRound;
+            if (round > 0 && !mbar_wait(&pace, (round - 1) & 1, &abort_flag)) {
+                ok = false;
+                ++done;
+                break;
+            }
+            if (lane == 0) mbar_arrive(&pace);
+        }
+    }
+    if (ok) {  // this warp's last round: the others no longer count on it
+        const int round = n_my > 0 ? (n_my - 1) / kRound : 0;
+        if (round > 0) ok = mbar_wait(&pace, (round - 1) & 1, &abort_flag);
+        if (ok && lane == 0) mbar_arrive_drop(&pace);
     }
     if (!ok) {  // a wait ran out: let the copies in flight land (each wait limited again), then leave
         if (lane == 0) raise_device_error(a.err, kErrTimeout);
@@ -675,114 +734,104 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
             phase ^= 1u << s;
         }
     } else if (row >= 0) {
-        finish_row(true);
+        finish_row(true, tiles, tile0);
     }
 
     // ---- pieces of the CTA, row by row
     __syncthreads();
     if (abort_flag) return;
-    if (threadIdx.x == 0) {
-        int n = 0, prev = -2;
-        for (int i = 0; i < 2 * kWarps; ++i) {
-            if (pieces[i].row < 0) continue;
-            if (pieces[i].row != prev) group_begin[n++] = i, prev = pieces[i].row;
-        }
-        group_begin[n] = 2 * kWarps;
-        n_groups = n;
+    if (warp == 0) {  // the pieces there are, in order; those of one row follow one another
+        const int r = lane < 2 * kWarps ? pieces[lane].row : -1;
+        const uint32_t have = __ballot_sync(kFull, r >= 0);
+        const int at = __popc(have & lanemask_lt());
+        const uint32_t before = have & lanemask_lt();
+        const int prev = __shfl_sync(kFull, r, before ? 31 - __clz(before) : 0);
+        const uint32_t starts = __ballot_sync(kFull, r >= 0 && (before == 0 || prev != r));
+        const int gi = __popc(starts & (lanemask_lt() | (1u << lane))) - 1;
+        if (r >= 0) piece_list[at] = lane;
+        if (starts >> lane & 1u) group_begin[gi] = at;
+        if (lane < 2 * kWarps) group_flags[lane] = 0;
+        __syncwarp();
+        if (r >= 0) atomicOr(&group_flags[gi], pieces[lane].flags);
+        if (lane == 0) n_groups = __popc(starts), group_begin[__popc(starts)] = __popc(have);
     }
     __syncthreads();
     auto piece_rec = [&](int i, int h) -> const float* {
         return (i & 1) ? reinterpret_cast<const float*>(ring + static_cast<size_t>(i >> 1) * stages * S::stage_bytes) + h * rec
                        : a.firsts + ((static_cast<size_t>(blockIdx.x) * kWarps + (i >> 1)) * heads + h) * rec;
     };
-    // the row's first tile among all and its number of tiles
-    auto locate = [&](int r, long long& tile0, int& tiles) {
-        const int item = r / part.mult;
-        const int c = item / chunk;
-        tile0 = prefix[c];
-        for (int i = c * chunk; i < item; ++i) tile0 += static_cast<long long>(tiles_of(item_entries(i))) * part.mult;
-        tiles = tiles_of(item_entries(item));
-        tile0 += static_cast<long long>(r % part.mult) * tiles;
-    };
     auto row_out = [&](int r) { return a.out + (static_cast<size_t>(r / nvg) * g.nvk + r % nvg * NVU) * g.Gv * DV; };
-    for (int w = warp; w < n_groups * heads; w += kWarps) {
-        const int gi = w / heads, h = w % heads;
-        const int i0 = group_begin[gi], i1 = group_begin[gi + 1], r = pieces[i0].row;
-        float M = -kInf, L = 0.f, o[DV / 32] = {};
-        int flags = 0;
-        for (int i = i0; i < i1; ++i)
-            if (pieces[i].row == r) {
-                M = fmaxf(M, piece_rec(i, h)[0]);
-                flags |= pieces[i].flags;
+    constexpr int LD = DV / 4;  // threads of a head, 4 dims each
+    bool crosses = false;       // a row of this CTA's goes on in another
+    for (int gi = 0; gi < n_groups; ++gi) {
+        const int i0 = group_begin[gi], i1 = group_begin[gi + 1];
+        const bool whole = group_flags[gi] == 3;
+        const Piece first = pieces[piece_list[i0]];
+        crosses |= !whole;
+        for (int t = threadIdx.x; t < heads * LD; t += kThreads) {
+            const int h = t / LD, d4 = t % LD;
+            float M = kNone, L = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int i = i0; i < i1; ++i) M = fmaxf(M, piece_rec(piece_list[i], h)[0]);
+#pragma unroll 4
+            for (int i = i0; i < i1; ++i) {
+                const float* src = piece_rec(piece_list[i], h);
+                const float2 head = *reinterpret_cast<const float2*>(src);
+                const float4 v = reinterpret_cast<const float4*>(src + kPagedRecHeader)[d4];
+                const float f = exp2_approx(head.x - M);
+                L += f * head.y;
+                o.x += f * v.x, o.y += f * v.y, o.z += f * v.z, o.w += f * v.w;
             }
-        for (int i = i0; i < i1; ++i)
-            if (pieces[i].row == r) {
-                const float* src = piece_rec(i, h);
-                const float f = src[0] == -kInf ? 0.f : exp2_approx(src[0] - M);
-                L += f * src[1];
-#pragma unroll
-                for (int d = 0; d < DV / 32; ++d) o[d] += f * src[kPagedRecHeader + lane + 32 * d];
+            if (whole) {
+                const float inv = L > 0.f ? 1.f / L : 0.f;
+                reinterpret_cast<float4*>(row_out(first.row) + h * DV)[d4] = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+            } else {
+                float* dst = a.records + ((static_cast<size_t>(blockIdx.x) * 2 + (first.tile0 < cta0 ? 0 : 1)) * heads + h) * rec;
+                if (d4 == 0) *reinterpret_cast<float2*>(dst) = make_float2(M, L);
+                reinterpret_cast<float4*>(dst + kPagedRecHeader)[d4] = o;
             }
-        if (flags == 3) {
-            float* dst = row_out(r) + h * DV;
-#pragma unroll
-            for (int d = 0; d < DV / 32; ++d) dst[lane + 32 * d] = L > 0.f ? o[d] / L : 0.f;
-        } else {
-            long long tile0;
-            int tiles;
-            locate(r, tile0, tiles);
-            float* dst = a.records + ((static_cast<size_t>(blockIdx.x) * 2 + (tile0 < cta0 ? 0 : 1)) * heads + h) * rec;
-            if (lane == 0) dst[0] = M, dst[1] = L;
-#pragma unroll
-            for (int d = 0; d < DV / 32; ++d) dst[kPagedRecHeader + lane + 32 * d] = o[d];
         }
     }
+    if (!crosses) return;
+    // the last CTA of a row that crosses CTAs merges its records
     __threadfence();
     __syncthreads();
-    // the last CTA of a row that crosses CTAs merges its records
     if (threadIdx.x < n_groups) {
-        const int i0 = group_begin[threadIdx.x], i1 = group_begin[threadIdx.x + 1], r = pieces[i0].row;
-        int flags = 0;
-        for (int i = i0; i < i1; ++i) flags |= pieces[i].row == r ? pieces[i].flags : 0;
-        int last = 0;
-        if (flags != 3) {
-            long long tile0;
-            int tiles;
-            locate(r, tile0, tiles);
-            const int n = cta_of_tile(tile0 + tiles - 1, part.T, part.C) - cta_of_tile(tile0, part.T, part.C) + 1;
-            last = atomicAdd(a.tickets + r, 1u) == static_cast<unsigned>(n - 1);
-            if (last) a.tickets[r] = 0u;
+        const Piece p = pieces[piece_list[group_begin[threadIdx.x]]];
+        int n = 0;
+        if (group_flags[threadIdx.x] != 3) {
+            n = cta_of_tile(p.tile0 + p.tiles - 1, part.T, part.C) - cta_of_tile(p.tile0, part.T, part.C) + 1;
+            if (atomicAdd(a.tickets + p.row, 1u) == static_cast<unsigned>(n - 1)) a.tickets[p.row] = 0u;
+            else n = 0;
         }
-        group_last[threadIdx.x] = last;
+        group_last[threadIdx.x] = n;  // records to merge, if this is the last CTA
     }
     __syncthreads();
     for (int gi = 0; gi < n_groups; ++gi) {
-        if (!group_last[gi]) continue;
+        const int n = group_last[gi];
+        if (n == 0) continue;
         __threadfence();
-        const int r = pieces[group_begin[gi]].row;
-        long long tile0;
-        int tiles;
-        locate(r, tile0, tiles);
-        const int first = cta_of_tile(tile0, part.T, part.C), n = cta_of_tile(tile0 + tiles - 1, part.T, part.C) - first + 1;
-        // 4 dims a lane, 32 / (DV / 4) records at a time
-        constexpr int LD = DV / 4, RP = 32 / LD;
+        const Piece p = pieces[piece_list[group_begin[gi]]];
+        const int first = cta_of_tile(p.tile0, part.T, part.C);
+        constexpr int RP = 32 / LD;  // records at a time
         const int sub = lane / LD, d4 = lane % LD;
         for (int h = warp; h < heads; h += kWarps) {
             auto record = [&](int i) {
                 return a.records + ((static_cast<size_t>(first + i) * 2 + (i == 0 ? 1 : 0)) * heads + h) * rec;
             };
-            float M = -kInf;
+            float M = kNone;
             for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(record(i)));
             M = warp_max(M);
             float L = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
             for (int i = sub; i < n; i += RP) {
                 const float* src = record(i);
-                const float mm = __ldcg(src), ll = __ldcg(src + 1);
+                const float2 head = __ldcg(reinterpret_cast<const float2*>(src));
                 const float4 v = __ldcg(reinterpret_cast<const float4*>(src + kPagedRecHeader) + d4);
-                const float f = mm == -kInf ? 0.f : exp2_approx(mm - M);
-                L += f * ll;
+                const float f = exp2_approx(head.x - M);
+                L += f * head.y;
                 o.x += f * v.x, o.y += f * v.y, o.z += f * v.z, o.w += f * v.w;
             }
 #pragma unroll
@@ -793,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
             }
             const float inv = L > 0.f ? 1.f / L : 0.f;
             if (sub == 0)
-                reinterpret_cast<float4*>(row_out(r) + h * DV)[d4] = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+                reinterpret_cast<float4*>(row_out(p.row) + h * DV)[d4] = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
         }
     }
 }
@@ -801,15 +850,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, DV, CW, NVU>::MINB))
 template <int DK, int DV, int CW, int NVU, int P>
 cudaError_t run(const PagedDecodeArgs& a, int sms, cudaStream_t stream) {
     using S = Shape<DK, DV, CW, NVU>;
-    int stages = (S::MINB == 2 ? kHalfRing : kWholeRing) / (kWarps * S::stage_bytes);
-    stages = stages > kMaxStages ? kMaxStages : stages;
-    const int smem = kWarps * stages * S::stage_bytes;
+    constexpr int smem = S::W * S::stages * S::stage_bytes;
     auto kern = paged_decode_kernel<DK, DV, CW, NVU, P>;
     const cudaError_t e = allow_dynamic_smem(kern, smem);
     if (e != cudaSuccess) return e;
-    int ctas = sms * S::MINB;
-    if (ctas > kPagedMaxCtas) ctas = kPagedMaxCtas;
-    return launch_dependent(kern, dim3(ctas), dim3(kThreads), smem, stream, a, stages, kWarps);
+    const int ctas = sms < kPagedMaxCtas ? sms : kPagedMaxCtas;
+    return launch_dependent(kern, dim3(ctas), dim3(S::W * 32), smem, stream, a, S::W);
 }
 
 template <int DK, int DV, int CW, int NVU>
