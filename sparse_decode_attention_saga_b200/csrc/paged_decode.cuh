@@ -23,7 +23,7 @@
 // pieces of a row that crosses ranges are merged per CTA in shared memory and
 // across CTAs by the row's last one (a ticket, fixed order: results do not
 // depend on timing).  One CTA has an SM to itself, and its warps keep within
-// a round of two tiles of one another (a barrier that a warp arrives at after
+// a round of four tiles of one another (a barrier that a warp arrives at after
 // a round and waits for a round later): with two CTAs and no such pace the
 // SM's older warps ran first and left the younger ones to finish alone, at
 // half the issue rate (batch 16 x 128K: CTAs ended at 150 and at 215 us).
@@ -45,7 +45,7 @@ constexpr int kMaxStages = 4;
 constexpr uint32_t kFull = 0xffffffffu;
 // Shared memory for a CTA's rings (227 KB at most; the static part is below 10 KB).
 constexpr int kRingBytes = 216 * 1024;
-constexpr int kRound = 2;  // tiles between two arrivals at the pace barrier
+constexpr int kRound = 4;  // tiles between two arrivals at the pace barrier
 // A probability times its row's scale stands in fp16 in units of 2^-kUnit of the
 // largest scale: room for a logit to pass the accumulators' reference before a
 // new one is taken, when a product reaches 2^15.
