@@ -29,14 +29,17 @@ struct PagedGeom {
 
 SAGA_HD constexpr int paged_block_bytes(int P, int d) { return P * (d / 2 + 2); }
 
-// Offsets up to `scores` depend on the batch and head counts only; the
-// tickets are zero on entry and left at zero.
+// Offsets up to `scores` depend on the batch, the heads and their dims only;
+// the tickets are zero on entry and left at zero.
 struct PagedWsLayout {
     size_t err;      // uint32 sticky flag; word 2: the append's ticket (256-byte header)
     size_t tickets;  // uint32 [b*hv]
     size_t records;  // float  [kPagedMaxCtas][2][heads of a work row][dv + kPagedRecHeader]
     size_t firsts;   // float  [kPagedMaxCtas][kPagedWarps][heads of a work row][dv + kPagedRecHeader]
-    size_t scores;   // double [b*hk][max_pages]
+    size_t sel_tickets;  // uint32 [b*hk]
+    size_t row_max;      // uint32 [b*hk]  largest |bound| (bits of a float; zero on entry, left at zero)
+    size_t scores;   // float  [b*hk][max_pages]
+    size_t keys;     // uint64 [b*hk][max_pages]
     size_t total;
 };
 
@@ -65,10 +68,13 @@ inline PagedWsLayout paged_workspace_layout(const PagedGeom& g) {
     };
     w.err = take(256);
     w.tickets = take(static_cast<size_t>(g.b) * g.hv * sizeof(uint32_t));
+    w.sel_tickets = take(static_cast<size_t>(g.b) * g.hk * sizeof(uint32_t));
+    w.row_max = take(static_cast<size_t>(g.b) * g.hk * sizeof(uint32_t));
     const size_t rec = static_cast<size_t>(paged_row_shape(g).NVU) * g.Gv * (g.dv + kPagedRecHeader) * sizeof(float);
     w.records = take(kPagedMaxCtas * 2 * rec);
     w.firsts = take(static_cast<size_t>(kPagedMaxCtas) * kPagedWarps * rec);
-    w.scores = take(static_cast<size_t>(g.b) * g.hk * g.max_pages * sizeof(double));
+    w.scores = take(static_cast<size_t>(g.b) * g.hk * g.max_pages * sizeof(float));
+    w.keys = take(static_cast<size_t>(g.b) * g.hk * g.max_pages * sizeof(unsigned long long));
     w.total = off;
     return w;
 }
@@ -105,10 +111,13 @@ struct PagedSelectArgs {
     const int32_t* page_table;
     int32_t* sel;      // [b][hk][n_sel]
     int32_t* sel_cnt;  // [b][hk]
-    double* scores;
+    float* scores;
+    unsigned long long* keys;
+    uint32_t* tickets;
+    uint32_t* row_max;
     uint32_t* err;
 };
-cudaError_t launch_paged_select(const PagedSelectArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_paged_select(const PagedSelectArgs& a, cudaStream_t stream);
 
 struct PagedDecodeArgs {
     PagedGeom g;

@@ -179,10 +179,13 @@ int saga_paged_select(const saga_paged_dims* dims, int32_t n_sel, int32_t n_firs
     a.page_table = page_table;
     a.sel = sel_pages;
     a.sel_cnt = sel_cnt;
-    a.scores = ws_at<double>(ws, L.scores);
+    a.scores = ws_at<float>(ws, L.scores);
+    a.keys = ws_at<unsigned long long>(ws, L.keys);
+    a.tickets = ws_at<uint32_t>(ws, L.sel_tickets);
+    a.row_max = ws_at<uint32_t>(ws, L.row_max);
     a.err = ws_at<uint32_t>(ws, L.err);
-    note_launches(2);
-    return finish(launch_paged_select(a, sms, reinterpret_cast<cudaStream_t>(stream)));
+    note_launches(1);
+    return finish(launch_paged_select(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int saga_paged_decode(const saga_paged_dims* dims, const void* q, const void* k_pages, const void* v_pages,
