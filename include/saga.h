@@ -384,7 +384,8 @@ int saga_paged_read(const saga_paged_dims* dims, int32_t n_tokens, const int32_t
  *   q [batch, h_q, head_dim] bf16 (rotated)
  *   sel_pages [batch, h_k, n_sel] int32: page indices in the sequence,
  *   ascending; entries past sel_cnt are left as they were.
- *   sel_cnt [batch, h_k] int32: min(n_sel, the sequence's pages). */
+ *   sel_cnt [batch, h_k] int32: min(n_sel, the sequence's pages).
+ * max_pages is at most 262144 here (else SAGA_ERR_UNSUPPORTED). */
 int saga_paged_select(const saga_paged_dims* dims, int32_t n_sel, int32_t n_first, int32_t n_last,
                       const void* q, const void* bounds, const int32_t* seq_lens,
                       const int32_t* page_table, int32_t* sel_pages, int32_t* sel_cnt, void* ws,

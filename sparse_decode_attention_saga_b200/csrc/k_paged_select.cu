@@ -11,11 +11,13 @@
 // query heads a tile, straight from global memory (each bound is used once,
 // its fragment is 16 contiguous bytes per lane).  A score is off by less than
 // E = 2^-14 max_h sum|q| max|bound| (at most 16 tile products of 17 addends,
-// each cut at 2^-23 of the largest).  The row's last CTA then finds the n-th
-// largest fp32 score to within E; pages further than 2E above are in, further
-// below out, and only those between (a page or two, unless scores tie) are
-// scored again in 64 bits.  One launch; bound by the read of the bounds and,
-// in small batches, by the chain of the last CTA's steps.
+// each cut at 2^-23 of the largest).  The row's last CTA finds the bin of the
+// n-th largest fp32 score in a histogram over equal steps between the row's
+// extremes (again between the bin's own while it is full), which leaves an
+// interval [lo, hi] that the score lies in; pages 2E above it are in, pages 2E
+// below out, and only those between (a few, unless scores tie) are scored
+// again in 64 bits.  One launch; bound by the read of the bounds and, in small
+// batches, by the chain of the last CTA's steps.
 #include <cuda_bf16.h>
 
 #include "paged.h"
@@ -28,9 +30,11 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kChunk = kWarps * 16;  // pages scored by a CTA
-constexpr int kPer = 16;             // pages a thread holds in registers in the search
+constexpr int kPer = 16;             // pages a thread holds in registers
 constexpr int kRound = kThreads * kPer;
 constexpr int kBand = 1024;  // pages scored again in shared memory
+constexpr int kBins = 2048;
+constexpr int kFewInBin = 24;  // pages in the threshold's bin that need no finer histogram
 constexpr uint32_t kFull = 0xffffffffu;
 
 __device__ __forceinline__ unsigned long long double_to_key(double x) {
@@ -42,22 +46,7 @@ __device__ __forceinline__ unsigned long long double_to_key(double x) {
 __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); }
 __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
-// Sum over the block of up to three 10-bit counts per thread group packed in
-// one word per warp (each warp's below 1024); all threads get the sums.
-__device__ __forceinline__ int3 block_sum3(uint32_t packed, uint32_t (&buf)[2][kWarps], int& turn) {
-    packed = __reduce_add_sync(kFull, packed);
-    if ((threadIdx.x & 31) == 0) buf[turn][threadIdx.x >> 5] = packed;
-    __syncthreads();
-    int3 s = make_int3(0, 0, 0);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        const uint32_t v = buf[turn][w];
-        s.x += v & 1023u, s.y += (v >> 10) & 1023u, s.z += v >> 20;
-    }
-    turn ^= 1;  // the other buffer next: one barrier a round
-    return s;
-}
-
+// Sum over the block (two buffers in turn: one barrier a call).
 __device__ __forceinline__ int block_sum(int n, uint32_t (&buf)[2][kWarps], int& turn) {
     n = __reduce_add_sync(kFull, n);
     if ((threadIdx.x & 31) == 0) buf[turn][threadIdx.x >> 5] = n;
@@ -92,13 +81,27 @@ __device__ __forceinline__ int block_prefix(int n, int& total, uint32_t (&buf)[2
     return before + incl - n;
 }
 
+// The largest of v over the block (min: negate).
+__device__ __forceinline__ float block_max(float v, uint32_t (&buf)[2][kWarps], int& turn) {
+    v = warp_max(v);
+    if ((threadIdx.x & 31) == 0) buf[turn][threadIdx.x >> 5] = __float_as_uint(v);
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) v = fmaxf(v, __uint_as_float(buf[turn][w]));
+    turn ^= 1;
+    return v;
+}
+
 template <int DK, int NT>
-__global__ void __launch_bounds__(kThreads, 1) select_kernel(const PagedSelectArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) select_kernel(const PagedSelectArgs a) {
     constexpr int CH = DK / 32;  // 16-byte chunks of a bound row per lane
+    extern __shared__ uint32_t words[];  // the picked pages' bits, then each word's rank
     __shared__ uint32_t sums[2][kWarps];
+    __shared__ uint32_t bins[kBins];
     __shared__ int band_page[kBand];
     __shared__ unsigned long long band_key[kBand];
-    __shared__ int n_band, is_last;
+    __shared__ int n_band, is_last, the_bin, the_rank;
+    __shared__ uint32_t bin_lo, bin_hi;
     __shared__ float q_sum;
     pdl_wait();
     pdl_trigger();
@@ -126,6 +129,15 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const PagedSelectAr
     const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + (static_cast<size_t>(b) * g.hq + kh * g.Gk) * DK;
     const __nv_bfloat16* boxes = reinterpret_cast<const __nv_bfloat16*>(a.bounds);
     float* scores = a.scores + static_cast<size_t>(row) * g.max_pages;
+    if (threadIdx.x == 0) q_sum = 0.f, n_band = 0;
+    __syncthreads();
+    if (warp < g.Gk) {  // sum |q| of a head, the largest of them
+        float s = 0.f;
+#pragma unroll
+        for (int i = lane; i < DK; i += 32) s += fabsf(__bfloat162float(q[warp * DK + i]));
+        s = warp_sum(s);
+        if (lane == 0) atomicMax(reinterpret_cast<int*>(&q_sum), __float_as_int(s));
+    }
     const int p0 = blockIdx.x * kChunk + warp * 16;
     if (p0 < np) {
         uint4 lo[2][CH], hi[2][CH];
@@ -193,107 +205,139 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const PagedSelectAr
     // ---- the row's last CTA picks
     __threadfence();
     __syncthreads();
-    if (threadIdx.x == 0) {
-        is_last = atomicAdd(a.tickets + row, 1u) == static_cast<unsigned>(chunks - 1);
-        n_band = 0;
-        q_sum = 0.f;
-    }
+    if (threadIdx.x == 0) is_last = atomicAdd(a.tickets + row, 1u) == static_cast<unsigned>(chunks - 1);
     __syncthreads();
     if (!is_last) return;
     __threadfence();
-    // sum |q| per head, the largest
-    for (int h = warp; h < g.Gk; h += kWarps) {
-        float s = 0.f;
-#pragma unroll
-        for (int i = lane; i < DK; i += 32) s += fabsf(__bfloat162float(q[h * DK + i]));
-        s = warp_sum(s);
-        if (lane == 0) atomicMax(reinterpret_cast<int*>(&q_sum), __float_as_int(s));
-    }
+    const int n_words = (np + 31) / 32;
+    uint32_t* ranks = words + n_words;
     auto forced = [&](int p) { return p < a.n_first || p >= np - a.n_last; };
     const int want = a.n_sel - a.n_first - a.n_last;  // pages to pick beside the forced ones
-    // this thread's pages: 16 in a row per round, their keys in registers (the only round, as a rule)
+    // this thread's scores: every 512th page, 16 in registers (all there are, as a rule); no page: -inf
     const int rounds = (np + kRound - 1) / kRound;
-    uint32_t key[kPer];
-    auto load_keys = [&](int round) {
-        const int at = round * kRound + threadIdx.x * kPer;
+    float x[kPer];
+    auto load = [&](int round) {
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-            const int p = at + j;
-            key[j] = p < np && !forced(p) ? float_to_key(__ldcg(scores + p)) : 0u;
+            const int p = round * kRound + j * kThreads + threadIdx.x;
+            x[j] = p < np && !forced(p) ? __ldcg(scores + p) : -kInf;
+        }
+    };
+    auto each = [&](auto&& f) {  // f(score, page) for the pages that are not forced
+        for (int r = 0; r < rounds; ++r) {
+            if (rounds > 1) load(r);
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                const int p0j = r * kRound + j * kThreads;
+                if (p0j >= np) break;
+                const int p = p0j + threadIdx.x;
+                if (p < np && !forced(p)) f(x[j], p);
+            }
         }
     };
     int turn = 0;
-    load_keys(0);
-    __syncthreads();
+    load(0);
     const float margin = 2.f * 6.2e-5f * q_sum * __uint_as_float(__ldcg(a.row_max + row));  // 2E (2^-14 and its rounding)
-    // ---- the want-th largest key, two bits at a time, until the interval is within E
-    uint32_t t = 0;
-    int sh = 30;
-    for (;; sh -= 2) {
-        const uint32_t c1 = t | (1u << sh), c2 = t | (2u << sh), c3 = t | (3u << sh);
-        int3 n = make_int3(0, 0, 0);
-        for (int r = 0; r < rounds; ++r) {
-            if (rounds > 1) load_keys(r);
-            uint32_t packed = 0;
+    float top = -kInf, low = -kInf;
+    each([&](float s, int) {
+        if (s > -kInf) top = fmaxf(top, s), low = fmaxf(low, -s);
+    });
+    top = block_max(top, sums, turn);
+    low = -block_max(low, sums, turn);
+    // ---- the interval [lo, hi] of the want-th largest
+    float lo = -kInf, hi = kInf;
+    int rank = want;  // of it among the scores in (.., top]
+    for (int level = 0; level < 4 && want > 0; ++level) {
+        for (int i = threadIdx.x; i < kBins; i += kThreads) bins[i] = 0u;
+        if (threadIdx.x == 0) bin_lo = 0xffffffffu, bin_hi = 0u, the_bin = 0, the_rank = 1;
+        __syncthreads();
+        const float step = top > low ? (kBins - 1) / (top - low) : 0.f;
+        auto bin_of = [&](float s) { return static_cast<int>(fminf(fmaxf((s - low) * step, 0.f), kBins - 1.f)); };
+        auto in = [&](float s) { return s >= lo && s <= hi; };  // of the level above's bin
+        each([&](float s, int) {
+            if (in(s)) atomicAdd(&bins[bin_of(s)], 1u);
+        });
+        __syncthreads();
+        // bins from the top: thread i has the i-th four
+        uint32_t n[kBins / kThreads], sum = 0;
 #pragma unroll
-            for (int j = 0; j < kPer; ++j)
-                packed += (key[j] >= c1 ? 1u : 0u) + (key[j] >= c2 ? 1u << 10 : 0u) + (key[j] >= c3 ? 1u << 20 : 0u);
-            const int3 m = block_sum3(packed, sums, turn);
-            n.x += m.x, n.y += m.y, n.z += m.z;
+        for (int i = 0; i < kBins / kThreads; ++i) sum += n[i] = bins[kBins - 1 - (threadIdx.x * (kBins / kThreads) + i)];
+        int total;
+        int before = block_prefix(sum, total, sums, turn);
+#pragma unroll
+        for (int i = 0; i < kBins / kThreads; ++i) {
+            if (before < rank && before + static_cast<int>(n[i]) >= rank) {
+                the_bin = kBins - 1 - (threadIdx.x * (kBins / kThreads) + i);
+                the_rank = rank - before;
+            }
+            before += n[i];
         }
-        t = n.z >= want ? c3 : n.y >= want ? c2 : n.x >= want ? c1 : t;
-        if (sh == 0) break;
-        const float lo = key_to_float(t), hi = key_to_float(t | ((1u << sh) - 1u));
-        if (hi - lo <= 0.5f * margin) break;
+        __syncthreads();
+        const int bin = the_bin;
+        each([&](float s, int) {
+            if (in(s) && bin_of(s) == bin) {
+                atomicMin(&bin_lo, float_to_key(s));
+                atomicMax(&bin_hi, float_to_key(s));
+            }
+        });
+        __syncthreads();
+        const bool few = bins[bin] <= kFewInBin;
+        rank = the_rank;
+        lo = key_to_float(bin_lo);
+        hi = key_to_float(bin_hi);
+        top = hi, low = lo;
+        if (few || hi - lo <= 0.25f * margin) break;
+        __syncthreads();  // the bins are cleared next
     }
-    float cut_lo = key_to_float(t) - margin, cut_hi = key_to_float(t | ((1u << sh) - 1u)) + margin;
-    // (no page but the forced ones is wanted: none above the cut)
-    if (want == 0) cut_lo = cut_hi = kInf;
-    // ---- the pages above the cut, and those the fp32 scores leave open
+    float cut_lo = lo - margin, cut_hi = hi + margin;
+    if (want == 0) cut_lo = cut_hi = kInf;  // the forced pages only
+    // ---- the pages above the cut and the forced ones, and those that the fp32 scores leave open
+    for (int i = threadIdx.x; i < n_words; i += kThreads) words[i] = 0u;
+    __syncthreads();
     int above = 0;
     for (int r = 0; r < rounds; ++r) {
-        if (rounds > 1) load_keys(r);
-        int n = 0;
+        if (rounds > 1) load(r);
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-            if (key[j] == 0u) continue;
-            const float s = key_to_float(key[j]);
-            if (s > cut_hi) {
-                ++n;
-            } else if (s >= cut_lo) {
+            const int p0j = r * kRound + j * kThreads;
+            if (p0j >= np) break;
+            const int p = p0j + threadIdx.x;
+            const bool must = p < np && forced(p), over = p < np && !must && x[j] > cut_hi;
+            const uint32_t bits = __ballot_sync(kFull, must || over);
+            if (lane == 0 && p < np) words[p / 32] = bits;
+            above += over;
+            if (p < np && !must && !over && x[j] >= cut_lo) {
                 const int at = atomicAdd(&n_band, 1);
-                if (at < kBand) band_page[at] = r * kRound + threadIdx.x * kPer + j;
+                if (at < kBand) band_page[at] = p, band_key[at] = 0ull;
             }
         }
-        above += block_sum(n, sums, turn);
     }
-    __syncthreads();
+    above = block_sum(above, sums, turn);
+    auto set = [&](int p) { atomicOr(&words[p / 32], 1u << (p % 32)); };
     const int open = n_band, take = want - above;
-    // ---- open pages in 64 bits; the taken ones' scores become +inf, the others' -inf
-    auto exact_key = [&](int p) {  // by a warp
+    // ---- open pages in 64 bits
+    auto exact_score = [&](int p, int h) {  // of one head, by a warp (all lanes get it)
         const int phys = table[p];
-        double best = -static_cast<double>(kInf);
-        if (phys >= 0 && phys < g.n_pages) {
-            const __nv_bfloat16* box = boxes + (static_cast<size_t>(phys) * g.hk + kh) * 2 * DK;
-            for (int h = 0; h < g.Gk; ++h) {
-                double s = 0.0;
+        if (phys < 0 || phys >= g.n_pages) return -static_cast<double>(kInf);
+        const __nv_bfloat16* box = boxes + (static_cast<size_t>(phys) * g.hk + kh) * 2 * DK;
+        double s = 0.0;
 #pragma unroll
-                for (int i = lane; i < DK; i += 32) {
-                    const float x = __bfloat162float(q[h * DK + i]);
-                    s += static_cast<double>(fmaxf(x * __bfloat162float(box[i]), x * __bfloat162float(box[DK + i])));
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-                best = fmax(best, s);
-            }
+        for (int i = lane; i < DK; i += 32) {
+            const float v = __bfloat162float(q[h * DK + i]);
+            s += static_cast<double>(fmaxf(v * __bfloat162float(box[i]), v * __bfloat162float(box[DK + i])));
         }
-        return double_to_key(best);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+        return s;
     };
-    const bool all_open = open == take;
-    if (!all_open && open <= kBand) {
-        for (int i = warp; i < open; i += kWarps) {
-            const unsigned long long k = exact_key(band_page[i]);
-            if (lane == 0) band_key[i] = k;
+    if (open == take) {
+        each([&](float s, int p) {
+            if (s >= cut_lo && s <= cut_hi) set(p);
+        });
+    } else if (open <= kBand) {
+        for (int i = warp; i < open * g.Gk; i += kWarps) {
+            const unsigned long long k = double_to_key(exact_score(band_page[i / g.Gk], i % g.Gk));
+            if (lane == 0) atomicMax(&band_key[i / g.Gk], k);
         }
         __syncthreads();
         for (int i = threadIdx.x; i < open; i += kThreads) {
@@ -301,17 +345,15 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const PagedSelectAr
             const int p = band_page[i];
             int better = 0;
             for (int j = 0; j < open; ++j) better += band_key[j] > k || (band_key[j] == k && band_page[j] < p);
-            scores[p] = better < take ? kInf : -kInf;
+            if (better < take) set(p);
         }
-        __syncthreads();
-    } else if (!all_open) {  // many equal or nearly equal scores: their keys in the workspace, a search over 64 bits
+    } else {  // many equal or nearly equal scores: their keys in the workspace, a search over 64 bits
         unsigned long long* keys = a.keys + static_cast<size_t>(row) * g.max_pages;
-        auto is_open = [&](int p) {
-            const float s = __ldcg(scores + p);
-            return !forced(p) && s >= cut_lo && s <= cut_hi;
-        };
         for (int p = warp; p < np; p += kWarps) {
-            const unsigned long long k = is_open(p) ? exact_key(p) : 0ull;
+            const float s = __ldcg(scores + p);
+            unsigned long long k = 0ull;
+            if (!forced(p) && s >= cut_lo && s <= cut_hi)
+                for (int h = 0; h < g.Gk; ++h) k = max(k, double_to_key(exact_score(p, h)));
             if (lane == 0) keys[p] = k;
         }
         __syncthreads();
@@ -329,29 +371,24 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const PagedSelectAr
             const unsigned long long k = p < np ? keys[p] : 0ull;
             int total;
             const int before = block_prefix(k == cut && k != 0ull, total, sums, turn);
-            if (k != 0ull) scores[p] = k > cut || (k == cut && before < ties) ? kInf : -kInf;
+            if (k != 0ull && (k > cut || (k == cut && before < ties))) set(p);
             ties -= total;
         }
-        __syncthreads();
     }
-    // ---- the list, in order
-    const float least = all_open ? cut_lo : cut_hi;
-    int base = 0;
-    for (int r = 0; r < rounds; ++r) {
-        const int at = r * kRound + threadIdx.x * kPer;
-        uint32_t in = 0;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const int p = at + j;
-            if (p >= np) continue;
-            const float s = __ldcg(scores + p);
-            if (forced(p) || (want > 0 && (all_open ? s >= least : s > least))) in |= 1u << j;
-        }
+    __syncthreads();
+    // ---- the list, in order: each word's rank, then every picked page at its own
+    for (int w0 = 0, base = 0; w0 < n_words; w0 += kThreads) {
+        const int w = w0 + threadIdx.x;
         int total;
-        int to = base + block_prefix(__popc(in), total, sums, turn);
+        const int before = block_prefix(w < n_words ? __popc(words[w]) : 0, total, sums, turn);
+        if (w < n_words) ranks[w] = base + before;
         base += total;
-        for (; in; in &= in - 1, ++to)
-            if (to < a.n_sel) sel[to] = at + __ffs(in) - 1;
+    }
+    __syncthreads();
+    for (int p = threadIdx.x; p < np; p += kThreads) {
+        const uint32_t word = words[p / 32];
+        const int to = ranks[p / 32] + __popc(word & lanemask_lt());
+        if ((word >> (p % 32) & 1u) && to < a.n_sel) sel[to] = p;
     }
     if (threadIdx.x == 0) {
         a.sel_cnt[row] = a.n_sel;
@@ -371,7 +408,10 @@ cudaError_t launch_paged_select(const PagedSelectArgs& a, cudaStream_t stream) {
                           : (g.dk == 128  ? select_kernel<128, 2>
                              : g.dk == 64 ? select_kernel<64, 2>
                                           : select_kernel<32, 2>);
-    return launch_dependent(kern, grid, dim3(kThreads), 0, stream, a);
+    const int smem = (g.max_pages + 31) / 32 * 8;  // at most 64 KB (kPagedMaxSelectPages)
+    const cudaError_t e = allow_dynamic_smem(kern, smem);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kern, grid, dim3(kThreads), smem, stream, a);
 }
 
 }  // namespace saga

@@ -13,6 +13,8 @@ namespace saga {
 // the partial records).
 constexpr int kPagedMaxCtas = 160;
 constexpr int kPagedWarps = 16;
+// Pages of a sequence that the selection takes at most (their bits in shared memory).
+constexpr int kPagedMaxSelectPages = 1 << 18;
 // Partial record of one query head: largest logit (in powers of two), sum of
 // exponentials, two words of padding, o[dv].
 constexpr int kPagedRecHeader = 4;

@@ -164,6 +164,7 @@ int saga_paged_select(const saga_paged_dims* dims, int32_t n_sel, int32_t n_firs
         return SAGA_ERR_INVALID_ARG;
     if (!ok16(q) || !ok16(bounds) || !ok4(seq_lens) || !ok4(page_table) || !ok4(sel_pages) || !ok4(sel_cnt))
         return SAGA_ERR_INVALID_ARG;
+    if (g.max_pages > kPagedMaxSelectPages) return SAGA_ERR_UNSUPPORTED;
     if ((st = check_ws(g, ws, ws_bytes))) return st;
     int sms = 0;
     if ((st = require_device(&sms))) return st;
