@@ -10,8 +10,9 @@
 // Scores come from the tensor cores in bf16 with fp32 sums, 16 pages by 8
 // query heads a tile, straight from global memory (each bound is used once,
 // its fragment is 16 contiguous bytes per lane).  A score is off by less than
-// E = 2^-14 max_h sum|q| max|bound| (at most 16 tile products of 17 addends,
-// each cut at 2^-23 of the largest).  The row's last CTA finds the bin of the
+// E = 2^-14 max_h sum_d |q_d| max(|lo_d|, |hi_d|), which a third product gives
+// (at most 16 tile products of 17 addends, each cut at 2^-23 of the largest).
+// The row's last CTA finds the bin of the
 // n-th largest fp32 score in a histogram over equal steps between the row's
 // extremes (again between the bin's own while it is full), which leaves an
 // interval [lo, hi] that the score lies in; pages 2E above it are in, pages 2E
@@ -93,7 +94,7 @@ __device__ __forceinline__ float block_max(float v, uint32_t (&buf)[2][kWarps], 
 }
 
 template <int DK, int NT>
-__global__ void __launch_bounds__(kThreads, 2) select_kernel(const PagedSelectArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) select_kernel(const PagedSelectArgs a, const int groups) {
     constexpr int CH = DK / 32;  // 16-byte chunks of a bound row per lane
     extern __shared__ uint32_t words[];  // the picked pages' bits, then each word's rank
     __shared__ uint32_t sums[2][kWarps];
@@ -102,7 +103,6 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const PagedSelectAr
     __shared__ unsigned long long band_key[kBand];
     __shared__ int n_band, is_last, the_bin, the_rank;
     __shared__ uint32_t bin_lo, bin_hi;
-    __shared__ float q_sum;
     pdl_wait();
     pdl_trigger();
     const PagedGeom& g = a.g;
@@ -123,23 +123,26 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const PagedSelectAr
         }
         return;
     }
-    const int chunks = (np + kChunk - 1) / kChunk;
+    const int chunks = (np + groups * kChunk - 1) / (groups * kChunk);
     if (static_cast<int>(blockIdx.x) >= chunks) return;
     const int32_t* table = a.page_table + static_cast<size_t>(b) * g.max_pages;
     const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + (static_cast<size_t>(b) * g.hq + kh * g.Gk) * DK;
     const __nv_bfloat16* boxes = reinterpret_cast<const __nv_bfloat16*>(a.bounds);
     float* scores = a.scores + static_cast<size_t>(row) * g.max_pages;
-    if (threadIdx.x == 0) q_sum = 0.f, n_band = 0;
-    __syncthreads();
-    if (warp < g.Gk) {  // sum |q| of a head, the largest of them
-        float s = 0.f;
+    if (threadIdx.x == 0) n_band = 0;
+    // the queries' fragments, for hi, lo and the sum of magnitudes (k-steps of 16 dims: two to a lane's chunk)
+    uint4 qraw[NT][CH];
 #pragma unroll
-        for (int i = lane; i < DK; i += 32) s += fabsf(__bfloat162float(q[warp * DK + i]));
-        s = warp_sum(s);
-        if (lane == 0) atomicMax(reinterpret_cast<int*>(&q_sum), __float_as_int(s));
-    }
-    const int p0 = blockIdx.x * kChunk + warp * 16;
-    if (p0 < np) {
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            qraw[nt][c] = make_uint4(0u, 0u, 0u, 0u);
+            if (8 * nt + gq < g.Gk) qraw[nt][c] = *(reinterpret_cast<const uint4*>(q + (8 * nt + gq) * DK) + tq + 4 * c);
+        }
+    float size = 0.f;  // the largest sum of |q| max(|lo|, |hi|) over this lane's pages and heads
+    for (int group = 0; group < groups; ++group) {
+        const int p0 = ((blockIdx.x * groups + group) * kWarps + warp) * 16;
+        if (p0 >= np) break;
         uint4 lo[2][CH], hi[2][CH];
         bool bad[2];
 #pragma unroll
@@ -160,32 +163,31 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const PagedSelectAr
                 }
             }
         }
-        float d[NT][4] = {};
-        __nv_bfloat162 big = __float2bfloat162_rn(0.f);
-        const __nv_bfloat162 zero = big;
+        float d[NT][4] = {}, z[NT][4] = {};
+        const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+        auto larger = [](uint32_t x, uint32_t y) { return as_u32(__hmax2(__habs2(as_bf162(x)), __habs2(as_bf162(y)))); };
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const uint32_t l0[4] = {lo[0][c].x, lo[0][c].y, lo[0][c].z, lo[0][c].w}, l1[4] = {lo[1][c].x, lo[1][c].y, lo[1][c].z, lo[1][c].w};
             const uint32_t h0[4] = {hi[0][c].x, hi[0][c].y, hi[0][c].z, hi[0][c].w}, h1[4] = {hi[1][c].x, hi[1][c].y, hi[1][c].z, hi[1][c].w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                big = __hmax2(big, __hmax2(__habs2(as_bf162(l0[i])), __habs2(as_bf162(l1[i]))));
-                big = __hmax2(big, __hmax2(__habs2(as_bf162(h0[i])), __habs2(as_bf162(h1[i]))));
-            }
+            for (int s = 0; s < 2; ++s) {
+                const int i = 2 * s;
+                const uint32_t m0 = larger(l0[i], h0[i]), m1 = larger(l1[i], h1[i]);
+                const uint32_t m2 = larger(l0[i + 1], h0[i + 1]), m3 = larger(l1[i + 1], h1[i + 1]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (8 * nt + gq < g.Gk) v = *(reinterpret_cast<const uint4*>(q + (8 * nt + gq) * DK) + tq + 4 * c);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {  // a k-step of 16 dims: pairs 2s and 2s + 1 of each lane's chunk
-                    mma_16816(d[nt], l0[2 * s], l1[2 * s], l0[2 * s + 1], l1[2 * s + 1],
-                              as_u32(__hmin2(as_bf162(w[2 * s]), zero)), as_u32(__hmin2(as_bf162(w[2 * s + 1]), zero)));
-                    mma_16816(d[nt], h0[2 * s], h1[2 * s], h0[2 * s + 1], h1[2 * s + 1],
-                              as_u32(__hmax2(as_bf162(w[2 * s]), zero)), as_u32(__hmax2(as_bf162(w[2 * s + 1]), zero)));
+                for (int nt = 0; nt < NT; ++nt) {
+                    const uint32_t q0 = s ? qraw[nt][c].z : qraw[nt][c].x, q1 = s ? qraw[nt][c].w : qraw[nt][c].y;
+                    mma_16816(d[nt], l0[i], l1[i], l0[i + 1], l1[i + 1], as_u32(__hmin2(as_bf162(q0), zero)), as_u32(__hmin2(as_bf162(q1), zero)));
+                    mma_16816(d[nt], h0[i], h1[i], h0[i + 1], h1[i + 1], as_u32(__hmax2(as_bf162(q0), zero)), as_u32(__hmax2(as_bf162(q1), zero)));
+                    mma_16816(z[nt], m0, m1, m2, m3, q0 & 0x7fff7fffu, q1 & 0x7fff7fffu);
                 }
             }
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) size = fmaxf(size, z[nt][i]);
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             float s = -kInf;
@@ -199,9 +201,9 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const PagedSelectAr
             const int p = p0 + gq + 8 * r;
             if (tq == 0 && p < np) scores[p] = bad[r] ? -kInf : s;
         }
-        const float m = warp_max(fmaxf(__low2float(big), __high2float(big)));
-        if (lane == 0) atomicMax(a.row_max + row, __float_as_uint(m));  // not below 0: ordered as bits
     }
+    size = warp_max(size);
+    if (lane == 0 && size > 0.f) atomicMax(a.row_max + row, __float_as_uint(size));  // positive: ordered as bits
     // ---- the row's last CTA picks
     __threadfence();
     __syncthreads();
@@ -237,7 +239,8 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const PagedSelectAr
     };
     int turn = 0;
     load(0);
-    const float margin = 2.f * 6.2e-5f * q_sum * __uint_as_float(__ldcg(a.row_max + row));  // 2E (2^-14 and its rounding)
+    // 2E: 2^-14 of the row's largest size, itself within 2^-14
+    const float margin = 2.f * 6.2e-5f * __uint_as_float(__ldcg(a.row_max + row));
     float top = -kInf, low = -kInf;
     each([&](float s, int) {
         if (s > -kInf) top = fmaxf(top, s), low = fmaxf(low, -s);
@@ -316,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const PagedSelectAr
     auto set = [&](int p) { atomicOr(&words[p / 32], 1u << (p % 32)); };
     const int open = n_band, take = want - above;
     // ---- open pages in 64 bits
-    auto exact_score = [&](int p, int h) {  // of one head, by a warp (all lanes get it)
+    auto partial = [&](int p, int h) {  // this lane's share of a head's score
         const int phys = table[p];
         if (phys < 0 || phys >= g.n_pages) return -static_cast<double>(kInf);
         const __nv_bfloat16* box = boxes + (static_cast<size_t>(phys) * g.hk + kh) * 2 * DK;
@@ -326,8 +329,6 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const PagedSelectAr
             const float v = __bfloat162float(q[h * DK + i]);
             s += static_cast<double>(fmaxf(v * __bfloat162float(box[i]), v * __bfloat162float(box[DK + i])));
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
         return s;
     };
     if (open == take) {
@@ -335,9 +336,22 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const PagedSelectAr
             if (s >= cut_lo && s <= cut_hi) set(p);
         });
     } else if (open <= kBand) {
-        for (int i = warp; i < open * g.Gk; i += kWarps) {
-            const unsigned long long k = double_to_key(exact_score(band_page[i / g.Gk], i % g.Gk));
-            if (lane == 0) atomicMax(&band_key[i / g.Gk], k);
+        // a page and head per warp, four at a time (their loads and sums overlap)
+        const int pairs = open * g.Gk;
+        for (int i0 = warp; i0 < pairs; i0 += 4 * kWarps) {
+            double s[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = min(i0 + u * kWarps, pairs - 1);
+                s[u] = partial(band_page[i / g.Gk], i % g.Gk);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) s[u] += __shfl_xor_sync(kFull, s[u], o);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (lane == u && i0 + u * kWarps < pairs) atomicMax(&band_key[(i0 + u * kWarps) / g.Gk], double_to_key(s[u]));
         }
         __syncthreads();
         for (int i = threadIdx.x; i < open; i += kThreads) {
@@ -353,7 +367,12 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const PagedSelectAr
             const float s = __ldcg(scores + p);
             unsigned long long k = 0ull;
             if (!forced(p) && s >= cut_lo && s <= cut_hi)
-                for (int h = 0; h < g.Gk; ++h) k = max(k, double_to_key(exact_score(p, h)));
+                for (int h = 0; h < g.Gk; ++h) {
+                    double v = partial(p, h);
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+                    k = max(k, double_to_key(v));
+                }
             if (lane == 0) keys[p] = k;
         }
         __syncthreads();
@@ -399,9 +418,13 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const PagedSelectAr
 
 }  // namespace
 
-cudaError_t launch_paged_select(const PagedSelectArgs& a, cudaStream_t stream) {
+cudaError_t launch_paged_select(const PagedSelectArgs& a, int sms, cudaStream_t stream) {
     const PagedGeom& g = a.g;
-    const dim3 grid((g.max_pages + kChunk - 1) / kChunk, g.b * g.hk);
+    // 16-page groups per warp: one wave of CTAs where the batch needs no more
+    const int rows = g.b * g.hk, chunks = (g.max_pages + kChunk - 1) / kChunk;
+    int groups = static_cast<int>((static_cast<long long>(chunks) * rows + sms - 1) / sms);
+    groups = groups < 1 ? 1 : groups > 4 ? 4 : groups;
+    const dim3 grid((chunks + groups - 1) / groups, rows);
     auto kern = g.Gk <= 8 ? (g.dk == 128  ? select_kernel<128, 1>
                              : g.dk == 64 ? select_kernel<64, 1>
                                           : select_kernel<32, 1>)
@@ -411,7 +434,7 @@ cudaError_t launch_paged_select(const PagedSelectArgs& a, cudaStream_t stream) {
     const int smem = (g.max_pages + 31) / 32 * 8;  // at most 64 KB (kPagedMaxSelectPages)
     const cudaError_t e = allow_dynamic_smem(kern, smem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kern, grid, dim3(kThreads), smem, stream, a);
+    return launch_dependent(kern, grid, dim3(kThreads), smem, stream, a, groups);
 }
 
 }  // namespace saga

@@ -39,7 +39,7 @@ struct PagedWsLayout {
     size_t records;  // float  [kPagedMaxCtas][2][heads of a work row][dv + kPagedRecHeader]
     size_t firsts;   // float  [kPagedMaxCtas][kPagedWarps][heads of a work row][dv + kPagedRecHeader]
     size_t sel_tickets;  // uint32 [b*hk]
-    size_t row_max;      // uint32 [b*hk]  largest |bound| (bits of a float; zero on entry, left at zero)
+    size_t row_max;      // uint32 [b*hk]  largest size of a row's scores (bits of a float; zero on entry and exit)
     size_t scores;   // float  [b*hk][max_pages]
     size_t keys;     // uint64 [b*hk][max_pages]
     size_t total;
@@ -119,7 +119,7 @@ struct PagedSelectArgs {
     uint32_t* row_max;
     uint32_t* err;
 };
-cudaError_t launch_paged_select(const PagedSelectArgs& a, cudaStream_t stream);
+cudaError_t launch_paged_select(const PagedSelectArgs& a, int sms, cudaStream_t stream);
 
 struct PagedDecodeArgs {
     PagedGeom g;

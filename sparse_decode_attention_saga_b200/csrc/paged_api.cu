@@ -186,7 +186,7 @@ int saga_paged_select(const saga_paged_dims* dims, int32_t n_sel, int32_t n_firs
     a.row_max = ws_at<uint32_t>(ws, L.row_max);
     a.err = ws_at<uint32_t>(ws, L.err);
     note_launches(1);
-    return finish(launch_paged_select(a, reinterpret_cast<cudaStream_t>(stream)));
+    return finish(launch_paged_select(a, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int saga_paged_decode(const saga_paged_dims* dims, const void* q, const void* k_pages, const void* v_pages,
