@@ -205,12 +205,10 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const PagedSelectAr
     size = warp_max(size);
     if (lane == 0 && size > 0.f) atomicMax(a.row_max + row, __float_as_uint(size));  // positive: ordered as bits
     // ---- the row's last CTA picks
-    __threadfence();
     __syncthreads();
-    if (threadIdx.x == 0) is_last = atomicAdd(a.tickets + row, 1u) == static_cast<unsigned>(chunks - 1);
+    if (threadIdx.x == 0) is_last = take_ticket(a.tickets + row) == static_cast<unsigned>(chunks - 1);
     __syncthreads();
     if (!is_last) return;
-    __threadfence();
     const int n_words = (np + 31) / 32;
     uint32_t* ranks = words + n_words;
     auto forced = [&](int p) { return p < a.n_first || p >= np - a.n_last; };

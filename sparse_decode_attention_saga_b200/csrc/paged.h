@@ -15,10 +15,6 @@ constexpr int kPagedMaxCtas = 160;
 constexpr int kPagedWarps = 16;
 // Pages of a sequence that the selection takes at most (their bits in shared memory).
 constexpr int kPagedMaxSelectPages = 1 << 18;
-// Partial record of one query head: largest logit (in powers of two), sum of
-// exponentials, two words of padding, o[dv].
-constexpr int kPagedRecHeader = 4;
-
 struct PagedGeom {
     int b, hq, hk, hv, dk, dv;
     int P;          // positions per page: 16, 32 or 64
@@ -36,8 +32,8 @@ SAGA_HD constexpr int paged_block_bytes(int P, int d) { return P * (d / 2 + 2); 
 struct PagedWsLayout {
     size_t err;      // uint32 sticky flag; word 2: the append's ticket (256-byte header)
     size_t tickets;  // uint32 [b*hv]
-    size_t records;  // float  [kPagedMaxCtas][2][heads of a work row][dv + kPagedRecHeader]
-    size_t firsts;   // float  [kPagedMaxCtas][kPagedWarps][heads of a work row][dv + kPagedRecHeader]
+    size_t records;  // float  [kPagedMaxCtas][2][columns of a work row * (2 + dv)]
+    size_t firsts;   // float  [kPagedMaxCtas][kPagedWarps][columns of a work row * (2 + dv)]
     size_t sel_tickets;  // uint32 [b*hk]
     size_t row_max;      // uint32 [b*hk]  largest size of a row's scores (bits of a float; zero on entry and exit)
     size_t scores;   // float  [b*hk][max_pages]
@@ -72,7 +68,8 @@ inline PagedWsLayout paged_workspace_layout(const PagedGeom& g) {
     w.tickets = take(static_cast<size_t>(g.b) * g.hv * sizeof(uint32_t));
     w.sel_tickets = take(static_cast<size_t>(g.b) * g.hk * sizeof(uint32_t));
     w.row_max = take(static_cast<size_t>(g.b) * g.hk * sizeof(uint32_t));
-    const size_t rec = static_cast<size_t>(paged_row_shape(g).NVU) * g.Gv * (g.dv + kPagedRecHeader) * sizeof(float);
+    const PagedRowShape shape = paged_row_shape(g);
+    const size_t rec = static_cast<size_t>(shape.NVU) * shape.CW * (2 + g.dv) * sizeof(float);
     w.records = take(kPagedMaxCtas * 2 * rec);
     w.firsts = take(static_cast<size_t>(kPagedMaxCtas) * kPagedWarps * rec);
     w.scores = take(static_cast<size_t>(g.b) * g.hk * g.max_pages * sizeof(float));

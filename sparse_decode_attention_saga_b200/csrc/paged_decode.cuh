@@ -45,6 +45,9 @@ constexpr int kMaxStages = 4;
 constexpr uint32_t kFull = 0xffffffffu;
 // Shared memory for a CTA's rings (227 KB at most; the static part is below 10 KB).
 constexpr int kRingBytes = 216 * 1024;
+// Tiles of a CTA at least: fewer CTAs than SMs where there is less work, as each adds a record to merge
+// (batch 1 at 8K: 14.9 us at 16, 14.2 at 8, 14.8 at 4).
+constexpr int kMinTiles = 8;
 constexpr int kRound = 4;  // tiles between two arrivals at the pace barrier
 // A probability times its row's scale stands in fp16 in units of 2^-kUnit of the
 // largest scale: room for a logit to pass the accumulators' reference before a
@@ -169,8 +172,10 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
     constexpr int EPT = kTile / P;                                        // pages per tile
     constexpr int KBLK = paged_block_bytes(P, DK), VBLK = paged_block_bytes(P, DV);
     const int nvg = g.nvk / NVU;
-    const int heads = NVU * g.Gv;  // of a work row
-    const int rec = g.dv + kPagedRecHeader;
+    // A record of a work row: (reference, sum of exponentials) of its columns, then
+    // o as the lanes hold it, four values of each of the 32 lanes after another.
+    constexpr int kColumns = NVU * CW, NV = CW == 4 ? ACC * MT * 2 : ACC * MT * 4, kRecord = kColumns * (2 + DV);
+    static_assert(32 * NV == kColumns * DV, "every value once");
 
     if (lane < stages) mbar_init(&bars[warp][lane], 1);
     if (threadIdx.x == 0) mbar_init(&pace, kWarps);
@@ -419,39 +424,33 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
             else f[i] = v[x][i];
         }
     };
-    // o (times factor per column) of the current row to dst[head * stride + dim]
-    auto write_o = [&](const float (&factor)[NT][2], float* dst, int stride) {
-#pragma unroll
-        for (int x = 0; x < ACC; ++x) {
-            float f[2];
-            beside(factor, x, f);
-            if constexpr (CW == 4) {  // columns c and c + 4 are the two halves of one head: the left lanes add
-                                      // them up for dims 8 gq + 2 k, the right ones for 8 gq + 2 k + 1
-                const bool left = tq < 2;
-                const int hl = 2 * (tq & 1);
-                float* at = dst + (x * g.Gv + hl) * stride + 8 * gq + (left ? 0 : 1);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float mine = left ? acc[x][mt][i] : acc[x][mt][2 + i];
-                        const float other = left ? acc[x][mt][2 + i] : acc[x][mt][i];
-                        const float v = mine + __shfl_xor_sync(kFull, other, 2);
-                        if (hl + i < g.Gv) at[i * stride + 64 * (mt >> 2) + 2 * (mt & 3)] = v * f[i];
-                    }
-            } else {
-                const int hl = (CW == 16 ? 8 * x : 0) + 2 * tq;  // head of the value head
-                float* at = dst + ((CW == 16 ? 0 : x) * g.Gv + hl) * stride + 8 * gq;
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        if (hl + i < g.Gv)
-                            *reinterpret_cast<float2*>(at + i * stride + 64 * (mt >> 2) + 2 * (mt & 3)) =
-                                make_float2(acc[x][mt][i] * f[i], acc[x][mt][2 + i] * f[i]);
-            }
+    // The values of o that this lane has, NV of them: for CW 4 the sums of the
+    // two halves (columns c and c + 4 of a tile are one head; the left lanes
+    // add them up for dims 8 gq + 2 k, the right ones for 8 gq + 2 k + 1).
+    // Value k belongs to head (of the work row's columns) lane_head + head_at(k)
+    // and dim lane_dim + dim_at(k).
+    auto fragment = [&](int k) {
+        if constexpr (CW == 4) {
+            const int x = k / (2 * MT), mt = k / 2 % MT, i = k % 2;
+            const bool left = tq < 2;
+            const float mine = left ? acc[x][mt][i] : acc[x][mt][2 + i];
+            const float other = left ? acc[x][mt][2 + i] : acc[x][mt][i];
+            return mine + __shfl_xor_sync(kFull, other, 2);
+        } else {
+            return acc[k / (4 * MT)][k / 4 % MT][k % 4];
         }
     };
+    auto frag_head = [](int k) { return CW == 4 ? 4 * (k / (2 * MT)) + k % 2 : 8 * (k / (4 * MT)) + k % 2; };
+    auto frag_dim = [](int k) {
+        const int mt = CW == 4 ? k / 2 % MT : k / 4 % MT;
+        return 64 * (mt >> 2) + 2 * (mt & 3) + (CW == 4 ? 0 : k / 2 % 2);
+    };
+    auto lane_head = [](int ln) { return CW == 4 ? 2 * (ln & 1) : 2 * (ln & 3); };
+    auto lane_dim = [](int ln) { return 8 * (ln >> 2) + (CW == 4 ? (ln >> 1) & 1 : 0); };
+    // a column's place among the row's heads in the output, or -1
+    auto out_head = [&](int c) { return c % CW < g.Gv ? c / CW * g.Gv + c % CW : -1; };
+    auto row_out = [&](int r) { return a.out + (static_cast<size_t>(r / nvg) * g.nvk + r % nvg * NVU) * g.Gv * DV; };
+
     // (the row's number of tiles, and its first among all)
     auto finish_row = [&](bool end_of_range, int tiles, long long tile0) {
 #pragma unroll
@@ -460,28 +459,47 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) l[nt][i] += __shfl_xor_sync(kFull, l[nt][i], o);
-        const float unit = pow2i(expo - 127 - kUnit);
+        const float scale_unit = pow2i(expo - 127 - kUnit);
         float f[NT][2];
-        if (seen == 3) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) f[nt][i] = l[nt][i] > 0.f ? unit / l[nt][i] : 0.f;
-            write_o(f, a.out + (static_cast<size_t>(row / nvg) * g.nvk + row % nvg * NVU) * g.Gv * DV, DV);
-            return;
-        }
-        // an end of the range stays in this warp's ring (its copies are all in), an earlier piece goes to the workspace
-        float* dst = end_of_range ? reinterpret_cast<float*>(my_ring)
-                                  : a.firsts + (static_cast<size_t>(blockIdx.x) * kWarps + warp) * heads * rec;
+        const bool whole = seen == 3;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                f[nt][i] = unit;
-                const int h = head_of(nt, 2 * tq + i);
-                if (gq == 0 && h >= 0) dst[h * rec] = m[nt][i], dst[h * rec + 1] = l[nt][i];
+            for (int i = 0; i < 2; ++i) f[nt][i] = !whole ? scale_unit : l[nt][i] > 0.f ? scale_unit * __fdividef(1.f, l[nt][i]) : 0.f;
+        // an end of the range stays in this warp's ring (its copies are all in), an earlier piece goes to the workspace
+        float* dst = end_of_range ? reinterpret_cast<float*>(my_ring)
+                                  : a.firsts + (static_cast<size_t>(blockIdx.x) * kWarps + warp) * kRecord;
+        if (!whole && gq == 0) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (8 * nt + 2 * tq + i < kColumns)
+                        reinterpret_cast<float2*>(dst)[8 * nt + 2 * tq + i] = make_float2(m[nt][i], l[nt][i]);
+        }
+        float* to = row_out(row) + lane_dim(lane);
+        float fx[ACC][2];
+#pragma unroll
+        for (int x = 0; x < ACC; ++x) beside(f, x, fx[x]);
+#pragma unroll
+        for (int j = 0; j < NV / 4; ++j) {
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int k = 4 * j + i;
+                v[i] = fragment(k) * fx[CW == 4 ? k / (2 * MT) : k / (4 * MT)][k % 2];
             }
-        write_o(f, dst + kPagedRecHeader, rec);
+            if (whole) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int h = out_head(lane_head(lane) + frag_head(4 * j + i));
+                    if (h >= 0) to[h * DV + frag_dim(4 * j + i)] = v[i];
+                }
+            } else {
+                reinterpret_cast<float4*>(dst + 2 * kColumns)[j * 32 + lane] = make_float4(v[0], v[1], v[2], v[3]);
+            }
+        }
+        if (whole) return;
         if (lane == 0) {
             Piece& p = pieces[2 * warp + (end_of_range ? 1 : 0)];
             p.row = row;
@@ -682,24 +700,32 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
     };
 
     // ---- the warp's tiles
+    // (lanes leave a wait one by one: the vote brings the warp together again)
+    auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kFull, mbar_wait(bar, parity, &abort_flag)) != 0; };
     int produced = 0, done = 0, tiles = 0;
     long long tile0 = 0;
     uint32_t phase = 0;  // bit s: parity to wait for in stage s
     bool ok = true;
     for (; produced < stages && produced < n_my; ++produced) produce(produced);
-    for (int s = 0; done < n_my; ++done) {
-        if (!mbar_wait(&bars[warp][s], (phase >> s) & 1u, &abort_flag)) {
-            ok = false;
-            break;
+    for (int s = 0;; ++done) {
+        int4 meta = make_int4(-1, 0, 0, 0);
+        if (done < n_my) {
+            if (!(ok = warp_wait(&bars[warp][s], (phase >> s) & 1u))) break;
+            phase ^= 1u << s;
+            meta = *reinterpret_cast<const int4*>(&metas[warp][s]);
+        } else {  // the warp's last round is over: the others no longer count on it
+            const int round = n_my > 0 ? (n_my - 1) / kRound : 0;
+            if (round > 0 && !(ok = warp_wait(&pace, (round - 1) & 1))) break;
+            if (lane == 0) mbar_arrive_drop(&pace);
         }
-        phase ^= 1u << s;
-        const int4 meta = *reinterpret_cast<const int4*>(&metas[warp][s]);
         if (meta.x != row) {
-            if (row >= 0) finish_row(false, tiles, tile0);
+            if (row >= 0) finish_row(done == n_my, tiles, tile0);
+            if (done == n_my) break;
             begin_row(meta.x);
             tiles = meta.z;
             tile0 = w0 + done - meta.y;
         }
+        if (done == n_my) break;  // (a warp without a tile)
         seen |= (meta.y == 0 ? 1 : 0) | (meta.y == tiles - 1 ? 2 : 0);
         const uint8_t* buf = my_ring + s * S::stage_bytes;
 #pragma unroll
@@ -712,18 +738,12 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
         s = s + 1 == stages ? 0 : s + 1;
         if (done % kRound == kRound - 1 && done + 1 < n_my) {  // end of round done / kRound
             const int round = done / kRound;
-            if (round > 0 && !mbar_wait(&pace, (round - 1) & 1, &abort_flag)) {
-                ok = false;
+            if (round > 0 && !(ok = warp_wait(&pace, (round - 1) & 1))) {
                 ++done;
                 break;
             }
             if (lane == 0) mbar_arrive(&pace);
         }
-    }
-    if (ok) {  // this warp's last round: the others no longer count on it
-        const int round = n_my > 0 ? (n_my - 1) / kRound : 0;
-        if (round > 0) ok = mbar_wait(&pace, (round - 1) & 1, &abort_flag);
-        if (ok && lane == 0) mbar_arrive_drop(&pace);
     }
     if (!ok) {  // a wait ran out: let the copies in flight land (each wait limited again), then leave
         if (lane == 0) raise_device_error(a.err, kErrTimeout);
@@ -731,10 +751,9 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
         for (int i = done; i < produced; ++i) {
             const int s = i % stages;
             mbar_wait(&bars[warp][s], (phase >> s) & 1u, &given_up);
+            __syncwarp();
             phase ^= 1u << s;
         }
-    } else if (row >= 0) {
-        finish_row(true, tiles, tile0);
     }
 
     // ---- pieces of the CTA, row by row
@@ -756,53 +775,71 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
         if (lane == 0) n_groups = __popc(starts), group_begin[__popc(starts)] = __popc(have);
     }
     __syncthreads();
-    auto piece_rec = [&](int i, int h) -> const float* {
-        return (i & 1) ? reinterpret_cast<const float*>(ring + static_cast<size_t>(i >> 1) * stages * S::stage_bytes) + h * rec
-                       : a.firsts + ((static_cast<size_t>(blockIdx.x) * kWarps + (i >> 1)) * heads + h) * rec;
+    auto piece_rec = [&](int i) -> const float* {
+        return (i & 1) ? reinterpret_cast<const float*>(ring + static_cast<size_t>(i >> 1) * stages * S::stage_bytes)
+                       : a.firsts + (static_cast<size_t>(blockIdx.x) * kWarps + (i >> 1)) * kRecord;
     };
-    auto row_out = [&](int r) { return a.out + (static_cast<size_t>(r / nvg) * g.nvk + r % nvg * NVU) * g.Gv * DV; };
-    constexpr int LD = DV / 4;  // threads of a head, 4 dims each
-    bool crosses = false;       // a row of this CTA's goes on in another
+    // a thread's four values: place `at` of kPlaces in the records, of two columns
+    constexpr int kPlaces = kColumns * DV / 4;
+    auto columns_of = [&](int at, int (&c)[2]) {
+        c[0] = lane_head(at % 32) + frag_head(at / 32 * 4);
+        c[1] = c[0] + 1;
+    };
+    auto write_place = [&](int r, int at, const float (&v)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int k = at / 32 * 4 + i, h = out_head(lane_head(at % 32) + frag_head(k));
+            if (h >= 0) row_out(r)[h * DV + lane_dim(at % 32) + frag_dim(k)] = v[i];
+        }
+    };
+    bool crosses = false;  // a row of this CTA's goes on in another
     for (int gi = 0; gi < n_groups; ++gi) {
         const int i0 = group_begin[gi], i1 = group_begin[gi + 1];
         const bool whole = group_flags[gi] == 3;
         const Piece first = pieces[piece_list[i0]];
         crosses |= !whole;
-        for (int t = threadIdx.x; t < heads * LD; t += kThreads) {
-            const int h = t / LD, d4 = t % LD;
-            float M = kNone, L = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int i = i0; i < i1; ++i) M = fmaxf(M, piece_rec(piece_list[i], h)[0]);
+        for (int at = threadIdx.x; at < kPlaces; at += kThreads) {
+            int c[2];
+            columns_of(at, c);
+            float M[2] = {kNone, kNone}, L[2] = {0.f, 0.f}, o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
             for (int i = i0; i < i1; ++i) {
-                const float* src = piece_rec(piece_list[i], h);
-                const float2 head = *reinterpret_cast<const float2*>(src);
-                const float4 v = reinterpret_cast<const float4*>(src + kPagedRecHeader)[d4];
-                const float f = exp2_approx(head.x - M);
-                L += f * head.y;
-                o.x += f * v.x, o.y += f * v.y, o.z += f * v.z, o.w += f * v.w;
+                const float* src = piece_rec(piece_list[i]);
+                M[0] = fmaxf(M[0], src[2 * c[0]]);
+                M[1] = fmaxf(M[1], src[2 * c[1]]);
+            }
+#pragma unroll 4
+            for (int i = i0; i < i1; ++i) {
+                const float* src = piece_rec(piece_list[i]);
+                const float2 h0 = reinterpret_cast<const float2*>(src)[c[0]], h1 = reinterpret_cast<const float2*>(src)[c[1]];
+                const float4 v = reinterpret_cast<const float4*>(src + 2 * kColumns)[at];
+                const float f0 = exp2_approx(h0.x - M[0]), f1 = exp2_approx(h1.x - M[1]);
+                L[0] += f0 * h0.y, L[1] += f1 * h1.y;
+                o[0] += f0 * v.x, o[1] += f1 * v.y, o[2] += f0 * v.z, o[3] += f1 * v.w;
             }
             if (whole) {
-                const float inv = L > 0.f ? 1.f / L : 0.f;
-                reinterpret_cast<float4*>(row_out(first.row) + h * DV)[d4] = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+                const float i0f = L[0] > 0.f ? __fdividef(1.f, L[0]) : 0.f, i1f = L[1] > 0.f ? __fdividef(1.f, L[1]) : 0.f;
+                const float v[4] = {o[0] * i0f, o[1] * i1f, o[2] * i0f, o[3] * i1f};
+                write_place(first.row, at, v);
             } else {
-                float* dst = a.records + ((static_cast<size_t>(blockIdx.x) * 2 + (first.tile0 < cta0 ? 0 : 1)) * heads + h) * rec;
-                if (d4 == 0) *reinterpret_cast<float2*>(dst) = make_float2(M, L);
-                reinterpret_cast<float4*>(dst + kPagedRecHeader)[d4] = o;
+                float* dst = a.records + (static_cast<size_t>(blockIdx.x) * 2 + (first.tile0 < cta0 ? 0 : 1)) * kRecord;
+                reinterpret_cast<float4*>(dst + 2 * kColumns)[at] = make_float4(o[0], o[1], o[2], o[3]);
+                if (lane_dim(at % 32) < 2 && at / 32 * 4 % (NV / ACC) == 0) {  // one thread of a column pair (CW 4: either dim's)
+                    reinterpret_cast<float2*>(dst)[c[0]] = make_float2(M[0], L[0]);
+                    reinterpret_cast<float2*>(dst)[c[1]] = make_float2(M[1], L[1]);
+                }
             }
         }
     }
     if (!crosses) return;
-    // the last CTA of a row that crosses CTAs merges its records
-    __threadfence();
+    // ---- the last CTA of a row that crosses CTAs merges its records
     __syncthreads();
     if (threadIdx.x < n_groups) {
         const Piece p = pieces[piece_list[group_begin[threadIdx.x]]];
         int n = 0;
         if (group_flags[threadIdx.x] != 3) {
             n = cta_of_tile(p.tile0 + p.tiles - 1, part.T, part.C) - cta_of_tile(p.tile0, part.T, part.C) + 1;
-            if (atomicAdd(a.tickets + p.row, 1u) == static_cast<unsigned>(n - 1)) a.tickets[p.row] = 0u;
+            if (take_ticket(a.tickets + p.row) == static_cast<unsigned>(n - 1)) a.tickets[p.row] = 0u;
             else n = 0;
         }
         group_last[threadIdx.x] = n;  // records to merge, if this is the last CTA
@@ -811,39 +848,65 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
     for (int gi = 0; gi < n_groups; ++gi) {
         const int n = group_last[gi];
         if (n == 0) continue;
-        __threadfence();
         const Piece p = pieces[piece_list[group_begin[gi]]];
         const int first = cta_of_tile(p.tile0, part.T, part.C);
-        constexpr int RP = 32 / LD;  // records at a time
-        const int sub = lane / LD, d4 = lane % LD;
-        for (int h = warp; h < heads; h += kWarps) {
-            auto record = [&](int i) {
-                return a.records + ((static_cast<size_t>(first + i) * 2 + (i == 0 ? 1 : 0)) * heads + h) * rec;
+        auto record = [&](int i) { return a.records + (static_cast<size_t>(first + i) * 2 + (i == 0 ? 1 : 0)) * kRecord; };
+        // a place per thread; groups of threads take every kSubs-th record and are joined in the (free) rings
+        constexpr int kSubs = kThreads / kPlaces > 0 ? kThreads / kPlaces : 1;
+        float4* parts = reinterpret_cast<float4*>(ring);
+        const int sub = threadIdx.x / kPlaces;
+        for (int at = threadIdx.x % kPlaces; at < kPlaces && sub < kSubs; at += kThreads) {
+            int c[2];
+            columns_of(at, c);
+            float M[2] = {kNone, kNone}, L[2] = {0.f, 0.f}, o[4] = {0.f, 0.f, 0.f, 0.f};
+            auto join = [&](float2 h0, float2 h1, float4 v) {
+                const float m0 = fmaxf(M[0], h0.x), m1 = fmaxf(M[1], h1.x);
+                const float f0 = exp2_approx(h0.x - m0), f1 = exp2_approx(h1.x - m1);
+                const float g0 = exp2_approx(M[0] - m0), g1 = exp2_approx(M[1] - m1);
+                M[0] = m0, M[1] = m1;
+                L[0] = L[0] * g0 + f0 * h0.y, L[1] = L[1] * g1 + f1 * h1.y;
+                o[0] = o[0] * g0 + f0 * v.x, o[1] = o[1] * g1 + f1 * v.y;
+                o[2] = o[2] * g0 + f0 * v.z, o[3] = o[3] * g1 + f1 * v.w;
             };
-            float M = kNone;
-            for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(record(i)));
-            M = warp_max(M);
-            float L = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-            for (int i = sub; i < n; i += RP) {
-                const float* src = record(i);
-                const float2 head = __ldcg(reinterpret_cast<const float2*>(src));
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(src + kPagedRecHeader) + d4);
-                const float f = exp2_approx(head.x - M);
-                L += f * head.y;
-                o.x += f * v.x, o.y += f * v.y, o.z += f * v.z, o.w += f * v.w;
-            }
+            for (int i0 = sub; i0 < n; i0 += 8 * kSubs) {
+                float2 h0[8], h1[8];
+                float4 v[8];
 #pragma unroll
-            for (int s = LD; s < 32; s <<= 1) {
-                L += __shfl_xor_sync(kFull, L, s);
-                o.x += __shfl_xor_sync(kFull, o.x, s), o.y += __shfl_xor_sync(kFull, o.y, s);
-                o.z += __shfl_xor_sync(kFull, o.z, s), o.w += __shfl_xor_sync(kFull, o.w, s);
+                for (int u = 0; u < 8; ++u) {
+                    const int i = i0 + u * kSubs;
+                    h0[u] = h1[u] = make_float2(kNone, 0.f);
+                    v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (i < n) {
+                        const float* src = record(i);
+                        h0[u] = __ldcg(reinterpret_cast<const float2*>(src) + c[0]);
+                        h1[u] = __ldcg(reinterpret_cast<const float2*>(src) + c[1]);
+                        v[u] = __ldcg(reinterpret_cast<const float4*>(src + 2 * kColumns) + at);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u) join(h0[u], h1[u], v[u]);
             }
-            const float inv = L > 0.f ? 1.f / L : 0.f;
-            if (sub == 0)
-                reinterpret_cast<float4*>(row_out(p.row) + h * DV)[d4] = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+            if constexpr (kSubs > 1) {
+                if (sub > 0) {
+                    parts[(sub * kPlaces + at) * 2] = make_float4(o[0], o[1], o[2], o[3]);
+                    parts[(sub * kPlaces + at) * 2 + 1] = make_float4(M[0], L[0], M[1], L[1]);
+                }
+                named_barrier(1, kSubs * kPlaces);
+                if (sub == 0) {
+#pragma unroll
+                    for (int s = 1; s < kSubs; ++s) {
+                        const float4 h = parts[(s * kPlaces + at) * 2 + 1];
+                        join(make_float2(h.x, h.y), make_float2(h.z, h.w), parts[(s * kPlaces + at) * 2]);
+                    }
+                }
+            }
+            if (sub == 0) {
+                const float i0f = L[0] > 0.f ? __fdividef(1.f, L[0]) : 0.f, i1f = L[1] > 0.f ? __fdividef(1.f, L[1]) : 0.f;
+                const float v[4] = {o[0] * i0f, o[1] * i1f, o[2] * i0f, o[3] * i1f};
+                write_place(p.row, at, v);
+            }
         }
+        __syncthreads();  // the rings are used again
     }
 }
 
@@ -855,7 +918,7 @@ cudaError_t run(const PagedDecodeArgs& a, int sms, cudaStream_t stream) {
     const cudaError_t e = allow_dynamic_smem(kern, smem);
     if (e != cudaSuccess) return e;
     const int ctas = sms < kPagedMaxCtas ? sms : kPagedMaxCtas;
-    return launch_dependent(kern, dim3(ctas), dim3(S::W * 32), smem, stream, a, S::W);
+    return launch_dependent(kern, dim3(ctas), dim3(S::W * 32), smem, stream, a, kMinTiles);
 }
 
 template <int DK, int DV, int CW, int NVU>

@@ -38,6 +38,15 @@ __device__ __forceinline__ void pdl_trigger() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Takes a ticket: the block's writes before it (ordered by a block barrier)
+// are visible to whoever takes a later one, and theirs to this block after the
+// next barrier (read through L2).  Returns the tickets taken before.
+__device__ __forceinline__ uint32_t take_ticket(uint32_t* counter) {
+    uint32_t n;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(n) : "l"(counter) : "memory");
+    return n;
+}
+
 // ----------------------------------------------------------------- errors
 
 // Sticky device flag at the head of the workspace (read by
