@@ -793,12 +793,13 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
         }
     };
     bool crosses = false;  // a row of this CTA's goes on in another
-    for (int gi = 0; gi < n_groups; ++gi) {
-        const int i0 = group_begin[gi], i1 = group_begin[gi + 1];
-        const bool whole = group_flags[gi] == 3;
-        const Piece first = pieces[piece_list[i0]];
-        crosses |= !whole;
-        for (int at = threadIdx.x; at < kPlaces; at += kThreads) {
+    for (int gi = 0; gi < n_groups; ++gi) crosses |= group_flags[gi] != 3;
+    {
+        for (int item = threadIdx.x; item < n_groups * kPlaces; item += kThreads) {
+            const int gi = item / kPlaces, at = item % kPlaces;
+            const int i0 = group_begin[gi], i1 = group_begin[gi + 1];
+            const bool whole = group_flags[gi] == 3;
+            const Piece first = pieces[piece_list[i0]];
             int c[2];
             columns_of(at, c);
             float M[2] = {kNone, kNone}, L[2] = {0.f, 0.f}, o[4] = {0.f, 0.f, 0.f, 0.f};
