@@ -214,37 +214,6 @@ __device__ __forceinline__ Spread spread(int rows) {
     return Spread{grp % rp, grp / rp, rp, GROUPS / rp};
 }
 
-// Runs f(head, live, chunk a, chunk b) for this lane's heads of [h0, h1), every
-// warp of the CTA the same number of times (live: there is such a head and
-// row).  The chunks come through kDepth slots of the lane's own in shared
-// memory, filled asynchronously: loads in flight cost no registers.
-template <int D, class F>
-__device__ __forceinline__ void each_head(const __nv_bfloat16* src, int ca, int cb, bool row_live, const Spread& sp, int h0,
-                                          int h1, uint4 (*slots)[2][kThreads], F&& f) {
-    auto issue = [&](int slot, int hb) {
-        const bool ok = row_live && hb + sp.gh < h1;
-        const uint4* row = reinterpret_cast<const uint4*>(src + (ok ? (hb + sp.gh) * D : 0));
-        if (hb < h1 && ok) {
-            cp_async_16(smem_addr(&slots[slot][0][threadIdx.x]), row + ca, 16);
-            cp_async_16(smem_addr(&slots[slot][1][threadIdx.x]), row + cb, 16);
-        }
-        cp_async_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < kDepth; ++i) issue(i, h0 + i * sp.hp);
-    int slot = 0;
-    for (int hb = h0; hb < h1; hb += sp.hp) {
-        cp_async_wait<kDepth - 1>();
-        const bool live = row_live && hb + sp.gh < h1;
-        uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-        if (live) a = slots[slot][0][threadIdx.x], b = slots[slot][1][threadIdx.x];
-        f(hb + sp.gh, live, a, b);
-        issue(slot, hb + kDepth * sp.hp);
-        slot = slot + 1 == kDepth ? 0 : slot + 1;
-    }
-    cp_async_wait<0>();
-}
-
 // Eight values to the word of n + 8 (value i in bits 4i .. 4i+3) for the
 // scale s with reciprocal inv; 0x88888888 where s is 0.
 __device__ __forceinline__ uint32_t nibbles(const float (&y)[8], float s, float inv) {
@@ -270,89 +239,106 @@ __device__ __forceinline__ uint32_t nibbles(const float (&y)[8], float s, float 
 __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); }
 __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
-// Key or value rows of heads [h0, h1) of the unit into the pages.
-template <int D, int MODE, bool KEYS>
-__device__ __forceinline__ void write_rows(const PagedAppendArgs& a, const Unit& w, int h0, int h1,
+// The unit's rows of nk key heads from k0, nv value heads from v0 (rows of the
+// keys' width) and nq query heads from q0, one after another: keys and queries
+// rotated, keys and values rounded into the pages, queries to q_out.  A lane's
+// chunks come through kDepth slots of its own in shared memory, filled
+// asynchronously (loads in flight cost no registers).  One body for the three
+// kinds of rows: a short call is bound by fetching its instructions.
+struct Heads {
+    int k0, nk, v0, nv, q0, nq;
+};
+template <int D, int MODE>
+__device__ __forceinline__ void write_rows(const PagedAppendArgs& a, const Unit& w, const Heads& n, bool value_rows,
                                            uint32_t (*lo_hi)[2][D], uint4 (*slots)[2][kThreads]) {
     constexpr int LPR = D / 16;
     const PagedGeom& g = a.g;
     const Spread sp = spread<D>(w.rows);
-    const int heads = KEYS ? g.hk : g.hv, blk = KEYS ? g.kblk : g.vblk;
-    const long long stride = KEYS ? a.k_stride : a.v_stride;
-    uint8_t* block = (KEYS ? a.k_pages : a.v_pages) + static_cast<size_t>(w.phys) * heads * blk;
-    Pairs<D, MODE> pairs(a.rot);
-    for (int rb = 0; rb < w.rows; rb += sp.rp) {
-    const int r = rb + sp.r;
-    const bool row_live = r < w.rows;
-    if (row_live) pairs.load(a.rope, a.rot, w.page * g.P + w.off + r);
-    const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(KEYS ? a.k_new : a.v_new) + (w.token + r) * stride;
-    const int row_at = (w.off + r) * (D / 2), scale_at = g.P * (D / 2) + 2 * (w.off + r);
-    each_head<D>(src, pairs.ca, pairs.cb, row_live, sp, h0, h1, slots, [&](int h, bool live, uint4& va, uint4& vb) {
-        pairs.turn(va, vb);
-        float ya[8], yb[8], m = 0.f;
-        unpack8(va, ya);
-        unpack8(vb, yb);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(fabsf(ya[i]), fabsf(yb[i])));
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-        const __nv_bfloat16 scale = __float2bfloat16_rn(__fdiv_rn(m, 7.0f));
-        const float s = __bfloat162float(scale), inv = __fdividef(1.f, s);
-        const uint32_t wa = nibbles(ya, s, inv), wb = nibbles(yb, s, inv);
-        if (live) {
-            uint8_t* to = block + h * blk;
-            reinterpret_cast<uint32_t*>(to + row_at)[pairs.ca] = wa;
-            reinterpret_cast<uint32_t*>(to + row_at)[pairs.cb] = wb;
-            if (threadIdx.x % LPR == 0) *reinterpret_cast<__nv_bfloat16*>(to + scale_at) = scale;
-        }
-        if (KEYS && a.bounds) {  // this warp's rows of the head, then the CTA's
-            uint32_t lo[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w}, hi[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                hi[i] = row_live ? lo[i] : 0xff80ff80u;
-                lo[i] = row_live ? lo[i] : 0x7f807f80u;
-            }
-            const int span = min(32, sp.rp * LPR);
-            for (int o = LPR; o < span; o <<= 1)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    lo[i] = as_u32(__hmin2(as_bf162(lo[i]), as_bf162(__shfl_xor_sync(kFull, lo[i], o))));
-                    hi[i] = as_u32(__hmax2(as_bf162(hi[i]), as_bf162(__shfl_xor_sync(kFull, hi[i], o))));
-                }
-            if (h < h1 && (threadIdx.x & 31) % span < LPR) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int d = 8 * (i < 4 ? pairs.ca : pairs.cb) + 2 * (i & 3);
-                    atomicMin(&lo_hi[h - h0][0][d], float_to_key(bf16_lo(lo[i])));
-                    atomicMin(&lo_hi[h - h0][0][d + 1], float_to_key(bf16_hi(lo[i])));
-                    atomicMax(&lo_hi[h - h0][1][d], float_to_key(bf16_lo(hi[i])));
-                    atomicMax(&lo_hi[h - h0][1][d + 1], float_to_key(bf16_hi(hi[i])));
-                }
-            }
-        }
-    });
-    }
-}
-
-// Rotated queries of heads [h0, h1).
-template <int D, int MODE>
-__device__ __forceinline__ void write_queries(const PagedAppendArgs& a, const Unit& w, int h0, int h1,
-                                              uint4 (*slots)[2][kThreads]) {
-    const Spread sp = spread<D>(w.rows);
+    const int total = n.nk + n.nv + n.nq;
+    const size_t page_row = static_cast<size_t>(w.phys);
     Pairs<D, MODE> pairs(a.rot);
     for (int rb = 0; rb < w.rows; rb += sp.rp) {
         const int r = rb + sp.r;
         const bool row_live = r < w.rows;
-        if (row_live) pairs.load(a.rope, a.rot, w.page * a.g.P + w.off + r);
-        const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(a.q_new) + (w.token + r) * a.q_stride;
-        uint4* dst = reinterpret_cast<uint4*>(a.q_out) + static_cast<size_t>(w.token + r) * a.g.hq * (D / 8);
-        each_head<D>(src, pairs.ca, pairs.cb, row_live, sp, h0, h1, slots, [&](int h, bool live, uint4& va, uint4& vb) {
-            pairs.turn(va, vb);
-            if (live) {
-                dst[h * (D / 8) + pairs.ca] = va;
-                dst[h * (D / 8) + pairs.cb] = vb;
+        if (row_live && !value_rows) pairs.load(a.rope, a.rot, w.page * g.P + w.off + r);
+        const long long token = w.token + r;
+        const int row_at = (w.off + r) * (D / 2), scale_at = g.P * (D / 2) + 2 * (w.off + r);
+        auto issue = [&](int slot, int at) {
+            const int i = at + sp.gh;
+            if (row_live && i < total) {
+                const void* base = i < n.nk ? a.k_new : i < n.nk + n.nv ? a.v_new : a.q_new;
+                const long long stride = i < n.nk ? a.k_stride : i < n.nk + n.nv ? a.v_stride : a.q_stride;
+                const int h = i < n.nk ? n.k0 + i : i < n.nk + n.nv ? n.v0 + i - n.nk : n.q0 + i - n.nk - n.nv;
+                const uint4* row = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(base) + token * stride + h * D);
+                cp_async_16(smem_addr(&slots[slot][0][threadIdx.x]), row + pairs.ca, 16);
+                cp_async_16(smem_addr(&slots[slot][1][threadIdx.x]), row + pairs.cb, 16);
             }
-        });
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < kDepth; ++i) issue(i, i * sp.hp);
+        int slot = 0;
+        for (int at = 0; at < total; at += sp.hp) {  // every warp of the CTA the same number of times
+            cp_async_wait<kDepth - 1>();
+            const int i = at + sp.gh;
+            const bool live = row_live && i < total, key = i < n.nk, value = !key && i < n.nk + n.nv;
+            uint4 va = make_uint4(0u, 0u, 0u, 0u), vb = va;
+            if (live) va = slots[slot][0][threadIdx.x], vb = slots[slot][1][threadIdx.x];
+            if (MODE != kNoRotation && !value && !value_rows) pairs.turn(va, vb);
+            if (live && !key && !value) {
+                uint4* to = reinterpret_cast<uint4*>(a.q_out) + (static_cast<size_t>(token) * g.hq + n.q0 + i - n.nk - n.nv) * (D / 8);
+                to[pairs.ca] = va;
+                to[pairs.cb] = vb;
+            }
+            if (at < n.nk + n.nv) {  // rounding: keys or values among the CTA's heads of this time
+                float ya[8], yb[8], m = 0.f;
+                unpack8(va, ya);
+                unpack8(vb, yb);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) m = fmaxf(m, fmaxf(fabsf(ya[j]), fabsf(yb[j])));
+#pragma unroll
+                for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+                // (a seventh of 8 bits is at least a fourteenth of a step from every middle: the product rounds like the quotient)
+                const __nv_bfloat16 scale = __float2bfloat16_rn(m * 0.142857149f);
+                const float s = __bfloat162float(scale), inv = __fdividef(1.f, s);
+                const uint32_t wa = nibbles(ya, s, inv), wb = nibbles(yb, s, inv);
+                if (live && (key || value)) {
+                    const int heads = key ? g.hk : g.hv, h = key ? n.k0 + i : n.v0 + i - n.nk, blk = key ? g.kblk : g.vblk;
+                    uint8_t* to = (key ? a.k_pages : a.v_pages) + (page_row * heads + h) * blk;
+                    reinterpret_cast<uint32_t*>(to + row_at)[pairs.ca] = wa;
+                    reinterpret_cast<uint32_t*>(to + row_at)[pairs.cb] = wb;
+                    if (threadIdx.x % LPR == 0) *reinterpret_cast<__nv_bfloat16*>(to + scale_at) = scale;
+                }
+            }
+            if (a.bounds && at < n.nk) {  // this warp's rows of each key head, then the CTA's
+                uint32_t lo[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w}, hi[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    hi[j] = row_live ? lo[j] : 0xff80ff80u;
+                    lo[j] = row_live ? lo[j] : 0x7f807f80u;
+                }
+                const int span = min(32, sp.rp * LPR);
+                for (int o = LPR; o < span; o <<= 1)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        lo[j] = as_u32(__hmin2(as_bf162(lo[j]), as_bf162(__shfl_xor_sync(kFull, lo[j], o))));
+                        hi[j] = as_u32(__hmax2(as_bf162(hi[j]), as_bf162(__shfl_xor_sync(kFull, hi[j], o))));
+                    }
+                if (key && (threadIdx.x & 31) % span < LPR) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int d = 8 * (j < 4 ? pairs.ca : pairs.cb) + 2 * (j & 3);
+                        atomicMin(&lo_hi[i][0][d], float_to_key(bf16_lo(lo[j])));
+                        atomicMin(&lo_hi[i][0][d + 1], float_to_key(bf16_hi(lo[j])));
+                        atomicMax(&lo_hi[i][1][d], float_to_key(bf16_lo(hi[j])));
+                        atomicMax(&lo_hi[i][1][d + 1], float_to_key(bf16_hi(hi[j])));
+                    }
+                }
+            }
+            issue(slot, at + kDepth * sp.hp);
+            slot = slot + 1 == kDepth ? 0 : slot + 1;
+        }
+        cp_async_wait<0>();
     }
 }
 
@@ -379,11 +365,15 @@ __global__ void __launch_bounds__(kThreads, kResident) append_kernel(const Paged
                 (&lo_hi[0][0][0])[i] = (i / DK) & 1 ? 0u : 0xffffffffu;
             __syncthreads();
         }
-        if (h0 < k1) write_rows<DK, MODE, true>(a, w, h0, k1, lo_hi, slots);
         const int v0 = max(h0 - g.hk, 0), v1 = min(h1 - g.hk, g.hv);
-        if (v0 < v1) write_rows<DV, kNoRotation, false>(a, w, v0, v1, nullptr, slots);
         const int q0 = max(h0 - g.hk - g.hv, 0), q1 = h1 - g.hk - g.hv;
-        if (q0 < q1) write_queries<DK, MODE>(a, w, q0, q1, slots);
+        Heads n{h0, max(k1 - h0, 0), v0, max(v1 - v0, 0), q0, max(q1 - q0, 0)};
+        if constexpr (DK != DV) {  // narrower keys: the value rows on their own
+            const Heads values{0, 0, n.v0, n.nv, 0, 0};
+            n.nv = 0;
+            if (values.nv) write_rows<DV, kNoRotation>(a, w, values, true, nullptr, slots);
+        }
+        if (n.nk + n.nv + n.nq) write_rows<DK, MODE>(a, w, n, false, lo_hi, slots);
         if (bounds) {
             __syncthreads();
             __nv_bfloat16* box = reinterpret_cast<__nv_bfloat16*>(a.bounds) +
