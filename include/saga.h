@@ -308,7 +308,8 @@ int saga_cache_append(const saga_dims* dims, const void* k_new, const void* v_ne
  * a sequence's end and pages outside its table hold anything.
  * Supported shapes: head_dim = v_head_dim in {64, 128}, or 32 with 64; h_k in
  * {1, 2, 4, 8}; h_v a multiple of h_k, h_q of h_v, h_q/h_k <= 16, h_q <= 128;
- * page_size in {16, 32, 64}; batch*h_q <= 65535; max_pages*page_size <= 2^30.
+ * page_size in {16, 32, 64}; batch*h_q <= 65535; max_pages*page_size <= 2^30;
+ * at most 2^29 rows a call.
  * The conventions above (ownership, streams, workspace, validation) hold;
  * pointers of 32-bit values need 4-byte alignment only. */
 typedef struct {
@@ -337,7 +338,10 @@ typedef struct {
 } saga_rope;
 
 /* Bytes of workspace of the paged calls (0 for unsupported dims); zeroed once
- * by the caller, as above. */
+ * by the caller, as above.  It serves calls of one batch, head layout and head
+ * dims (page_size, max_pages and n_pages may change within its size); calls
+ * that share it, replayed graphs among them, are ordered on one stream.  After
+ * SAGA_ERR_TIMEOUT it is reset (saga_workspace_reset) before it is used again. */
 size_t saga_paged_workspace_bytes(const saga_paged_dims* dims);
 
 /* Appends n_tokens new rows: sequence b gets rows cu_new[b] .. cu_new[b+1]-1
@@ -357,7 +361,8 @@ size_t saga_paged_workspace_bytes(const saga_paged_dims* dims);
  * A page that the call writes to belongs to one sequence only.  Rows past
  * max_pages * page_size or whose position is not in the rotation table are
  * not written (nor their queries) and set the sticky flag; so is the whole
- * page's part of the run where one of its positions is past the table. */
+ * page's part of the run where one of its positions is past the table.
+ * q_out may be q_new itself (equal strides). */
 int saga_paged_append(const saga_paged_dims* dims, int32_t n_tokens, const int32_t* cu_new,
                       const int32_t* seq_lens, const int32_t* page_table, const void* k_new,
                       int64_t k_stride, const void* v_new, int64_t v_stride, const void* q_new,

@@ -244,12 +244,17 @@ def paged_workspace_bytes(d: SagaPagedDims) -> int:
     return int(load().saga_paged_workspace_bytes(ctypes.byref(d)))
 
 
+def _row_stride(t) -> int:
+    """Elements from one row to the next (of a single row: its own length)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
 def paged_append(d, n_tokens: int, cu_new, seq_lens, page_table, k_new, v_new, q_new, rope, k_pages, v_pages,
                  bounds, q_out, lens_out, ws, stream=None) -> None:
-    """rope: a SagaRope, or None.  Rows are stride(0) elements apart."""
+    """rope: a SagaRope, or None.  New rows [n_tokens, heads, dim] may be a stride apart."""
     _check("saga_paged_append", load().saga_paged_append(
         ctypes.byref(d), int(n_tokens), _ptr(cu_new), _ptr(seq_lens), _ptr(page_table), _ptr(k_new),
-        k_new.stride(0), _ptr(v_new), v_new.stride(0), _ptr(q_new), 0 if q_new is None else q_new.stride(0),
+        _row_stride(k_new), _ptr(v_new), _row_stride(v_new), _ptr(q_new), 0 if q_new is None else _row_stride(q_new),
         None if rope is None else ctypes.byref(rope), _ptr(k_pages), _ptr(v_pages), _ptr(bounds), _ptr(q_out),
         _ptr(lens_out), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
 

@@ -400,8 +400,9 @@ __global__ void __launch_bounds__(kThreads, kResident) append_kernel(const Paged
         __syncthreads();
         if (last)
             for (int i = threadIdx.x; i < g.b; i += kThreads) {
-                const int n = a.cu ? max(a.cu[i + 1] - a.cu[i], 0) : 1;
-                a.lens_out[i] = min(a.seq_lens[i] + n, g.max_pages * g.P);
+                const int len = a.seq_lens[i], t0 = a.cu ? a.cu[i] : 0, n = a.cu ? a.cu[i + 1] - t0 : 1;
+                const bool run = t0 >= 0 && n >= 0 && t0 <= a.n_tokens - n && len >= 0;  // else skipped and flagged
+                a.lens_out[i] = run ? min(len + n, max(len, g.max_pages * g.P)) : len;
             }
     }
 }

@@ -394,12 +394,13 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const PagedSelectAr
     }
     __syncthreads();
     // ---- the list, in order: each word's rank, then every picked page at its own
-    for (int w0 = 0, base = 0; w0 < n_words; w0 += kThreads) {
+    int picked = 0;
+    for (int w0 = 0; w0 < n_words; w0 += kThreads) {
         const int w = w0 + threadIdx.x;
         int total;
         const int before = block_prefix(w < n_words ? __popc(words[w]) : 0, total, sums, turn);
-        if (w < n_words) ranks[w] = base + before;
-        base += total;
+        if (w < n_words) ranks[w] = picked + before;
+        picked += total;
     }
     __syncthreads();
     for (int p = threadIdx.x; p < np; p += kThreads) {
@@ -408,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const PagedSelectAr
         if ((word >> (p % 32) & 1u) && to < a.n_sel) sel[to] = p;
     }
     if (threadIdx.x == 0) {
-        a.sel_cnt[row] = a.n_sel;
+        a.sel_cnt[row] = min(picked, a.n_sel);  // (n_sel, unless scores are no numbers)
         a.tickets[row] = 0u;
         a.row_max[row] = 0u;
     }

@@ -79,7 +79,7 @@ int saga_paged_append(const saga_paged_dims* dims, int32_t n_tokens, const int32
     PagedGeom g;
     int st = make_paged(dims, &g);
     if (st) return st;
-    if (n_tokens < 0 || n_tokens > (1 << 30) || (!cu_new && n_tokens != g.b)) return SAGA_ERR_INVALID_ARG;
+    if (n_tokens < 0 || n_tokens > (1 << 29) || (!cu_new && n_tokens != g.b)) return SAGA_ERR_INVALID_ARG;
     if ((cu_new && !aligned(cu_new, 4)) || !ok4(seq_lens) || !ok4(page_table) || (lens_out && !aligned(lens_out, 4)))
         return SAGA_ERR_INVALID_ARG;
     if (n_tokens) {
@@ -131,7 +131,7 @@ int saga_paged_read(const saga_paged_dims* dims, int32_t n_tokens, const int32_t
     PagedGeom g;
     int st = make_paged(dims, &g);
     if (st) return st;
-    if (n_tokens < 0 || n_tokens > (1 << 30) || (!cu && n_tokens != g.b)) return SAGA_ERR_INVALID_ARG;
+    if (n_tokens < 0 || n_tokens > (1 << 29) || (!cu && n_tokens != g.b)) return SAGA_ERR_INVALID_ARG;
     if ((cu && !aligned(cu, 4)) || !ok4(start) || !ok4(page_table)) return SAGA_ERR_INVALID_ARG;
     if (!ok16(k_pages) || !ok16(v_pages)) return SAGA_ERR_INVALID_ARG;
     if (n_tokens && (!ok16(k_out) || !ok16(v_out))) return SAGA_ERR_INVALID_ARG;

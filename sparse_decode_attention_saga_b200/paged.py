@@ -9,7 +9,9 @@ token of every sequence through append, select and decode.  Handing pages to
 sequences (filling ``page_table``) is the caller's, ``grow_table`` a helper for
 the plain case.  All compute runs in libsaga.so; calls only enqueue work on the
 current (or given) stream and follow lengths, table and lists on the device, so
-they can be captured in a CUDA graph (after one uncaptured call of each).
+they can be captured in a CUDA graph (after one uncaptured call of each).  What
+a call returns without an output buffer belongs to that stream.  Calls of one
+cache share its workspace and are ordered on one stream.
 """
 from __future__ import annotations
 
@@ -31,8 +33,7 @@ def _need(name, t, dtype, shape, device, rows=False):
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the cache on {device}")
     if not t.is_contiguous():
-        ok = rows and (t.shape[0] <= 1 or t.stride(0) >= t[0].numel()) and (t.shape[0] == 0 or t[0].is_contiguous())
-        if not ok or t.stride(0) % 8:
+        if not rows or not t[0].is_contiguous() or t.stride(0) < t[0].numel() or t.stride(0) % 8:
             raise ValueError(f"{name} must be contiguous" + (" in each row, rows a multiple of 8 elements apart"
                                                              if rows else ""))
 
@@ -83,6 +84,16 @@ class PagedCache:
         """The stream to enqueue on: the given one, or the cache's device's current one."""
         return torch.cuda.current_stream(self.device) if stream is None else stream
 
+    def _new(self, shape, dtype, stream, zero=False):
+        """A tensor made on the stream that the call runs on."""
+        make = torch.zeros if zero else torch.empty
+        if stream is None:
+            return make(shape, dtype=dtype, device=self.device)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=self.device)
+        with torch.cuda.stream(stream):
+            return make(shape, dtype=dtype, device=self.device)
+
     def _call(self, fn, *args, stream):
         if self.device.type == "cuda" and self.device.index != torch.cuda.current_device():
             with torch.cuda.device(self.device):
@@ -120,7 +131,7 @@ class PagedCache:
         if q_new is not None:
             _need("q_new", q_new, bf, (T, d.h_q, d.head_dim), dev, rows=True)
             if q_out is None:
-                q_out = torch.empty((T, d.h_q, d.head_dim), dtype=bf, device=dev)
+                q_out = self._new((T, d.h_q, d.head_dim), bf, stream)
             else:
                 _need("q_out", q_out, bf, (T, d.h_q, d.head_dim), dev)
         elif q_out is not None:
@@ -147,11 +158,11 @@ class PagedCache:
             _need("start", start, torch.int32, (d.batch,), dev)
         shapes = (n_tokens, d.h_k, d.head_dim), (n_tokens, d.h_v, self.dv)
         if k_out is None:
-            k_out = torch.empty(shapes[0], dtype=bf, device=dev)
+            k_out = self._new(shapes[0], bf, stream)
         else:
             _need("k_out", k_out, bf, shapes[0], dev)
         if v_out is None:
-            v_out = torch.empty(shapes[1], dtype=bf, device=dev)
+            v_out = self._new(shapes[1], bf, stream)
         else:
             _need("v_out", v_out, bf, shapes[1], dev)
         self._call(_lib.paged_read, d, n_tokens, cu, start, self.page_table, self.k_pages, self.v_pages, k_out, v_out,
@@ -165,11 +176,11 @@ class PagedCache:
         d, dev, i32 = self.dims, self.device, torch.int32
         _need("q", q, torch.bfloat16, (d.batch, d.h_q, d.head_dim), dev)
         if pages_out is None:
-            pages_out = torch.zeros((d.batch, d.h_k, n_sel), dtype=i32, device=dev)
+            pages_out = self._new((d.batch, d.h_k, n_sel), i32, stream, zero=True)
         else:
             _need("pages_out", pages_out, i32, (d.batch, d.h_k, n_sel), dev)
         if count_out is None:
-            count_out = torch.empty((d.batch, d.h_k), dtype=i32, device=dev)
+            count_out = self._new((d.batch, d.h_k), i32, stream)
         else:
             _need("count_out", count_out, i32, (d.batch, d.h_k), dev)
         self._call(_lib.paged_select, d, n_sel, first, last, q, self.bounds, self.seq_lens, self.page_table,
@@ -189,7 +200,7 @@ class PagedCache:
             _need("pages", pages, torch.int32, (d.batch, d.h_k, n_sel), dev)
             _need("count", count, torch.int32, (d.batch, d.h_k), dev)
         if out is None:
-            out = torch.empty((d.batch, d.h_q, self.dv), dtype=torch.float32, device=dev)
+            out = self._new((d.batch, d.h_q, self.dv), torch.float32, stream)
         else:
             _need("out", out, torch.float32, (d.batch, d.h_q, self.dv), dev)
         self._call(_lib.paged_decode, d, q, self.k_pages, self.v_pages, self.seq_lens, self.page_table, pages, count,

@@ -544,3 +544,130 @@ def test_launches_are_counted():
     n = _lib.launch_count()
     p.cache.decode(p.query().cuda())
     assert _lib.launch_count() == n + 1
+
+
+# ---------------------------------------------------------------- further shapes, streams and orders
+
+@pytest.mark.parametrize("layout", [(8, 2, 2, 64, 64), (16, 2, 8, 32, 64)])
+def test_many_short_sequences(layout):
+    """More sequences than a CTA has threads, most of them a few positions or none."""
+    rng = np.random.default_rng(3)
+    lens = [int(n) for n in rng.integers(0, 40, 1100)]
+    lens[7], lens[600] = 900, 333
+    lens[1099] = 0
+    p = filled(layout, 16, lens, 22)
+    q = p.query()
+    p.check_decode(q)
+    lists = [[rng.permutation(-(-n // 16))[:rng.integers(0, 3)].tolist() for _ in range(layout[1])] for n in lens]
+    lists[0][0] = []
+    p.check_decode(q, lists)
+
+
+def test_select_over_many_pages():
+    """A row longer than what the search holds in registers, next to short ones."""
+    lens = [16 * 20000 + 5, 100, 16 * 9000]
+    p = filled((4, 1, 2, 64, 64), 16, lens, 23)
+    q = p.query()
+    for n_sel in (3, 700):
+        want = ref.select(f64(q), p.state["bounds"], lens, p.state["page_table"], 16, n_sel, 1, 1)
+        pages, count = p.cache.select(q.cuda(), n_sel, 1, 1)
+        for b in range(3):
+            assert pages[b, 0, :count[b, 0]].tolist() == want[b][0]
+    q = torch.zeros(3, 4, 64, dtype=torch.bfloat16)  # every score equal
+    pages, _ = p.cache.select(q.cuda(), 9, 1, 1)
+    assert pages[0, 0].tolist() == list(range(8)) + [20000]
+    assert pages[2, 0].tolist() == list(range(8)) + [8999]
+
+
+def test_select_outlying_scores():
+    """A few pages far above the rest, equal runs among them, and bounds that cancel (score 0)."""
+    p = filled((4, 1, 2, 64, 64), 32, [32 * 600], 24)
+    box = p.state["bounds"]
+    table = p.state["page_table"][0]
+    for i in range(0, 600, 50):
+        box[table[i]] *= 1024.0
+    for i in range(100, 140):
+        box[table[i]] = box[table[100]]
+    box[table[300]] = 0.0
+    box[:] = ref.bf16(box)
+    p.cache.bounds.copy_(torch.from_numpy(box))
+    q = p.query()
+    for n_sel, first, last in ((5, 0, 0), (13, 1, 1), (40, 0, 2), (599, 0, 0)):
+        want = ref.select(f64(q), box, [19200], p.state["page_table"], 32, n_sel, first, last)
+        pages, count = p.cache.select(q.cuda(), n_sel, first, last)
+        assert pages[0, 0].tolist() == want[0][0] and count.tolist() == [[n_sel]]
+
+
+def test_every_call_on_another_stream_allocates_there():
+    """Outputs that the calls make themselves, on a side stream whose work lags behind the current one's."""
+    layout = (32, 4, 8, 64, 64)
+    a, b = filled(layout, 16, [700, 90], 25), filled(layout, 16, [700, 90], 25)
+    k, v, q = (t.cuda() for t in a.rows(2))
+    want = b.cache.step(k, v, q, 5)
+    start = b.cache.seq_lens - 1
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(2_000_000)
+    got = a.cache.step(k, v, q, 5, stream=side)
+    pages, count = a.cache.select(q, 5, stream=side.cuda_stream)
+    rows = a.cache.read(2, start=start, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+    assert all(torch.equal(x, y) for x, y in zip(rows, b.cache.read(2, start=start)))
+    want_pages, want_count = b.cache.select(q, 5)
+    assert torch.equal(pages, want_pages) and torch.equal(count, want_count)
+
+
+def test_append_rotates_in_place_and_takes_single_rows_of_any_stride():
+    p = Pair((12, 1, 2, 128, 128), 16, [40], [7], 26)
+    k, v, q = p.rows(1)
+    cu = np.array([0, 1], np.int32)
+    want = ref.append(p.state, f64(k), f64(v), f64(q), cu, p.table.numpy(), p.rot, False)
+    odd = torch.empty(1, 12, 128, dtype=torch.bfloat16, device="cuda").as_strided((1, 12, 128), (3, 128, 1))
+    odd.copy_(q)
+    assert p.cache.append(k.cuda(), v.cuda(), odd, q_out=odd) is odd
+    assert np.array_equal(f64(odd), want)
+    p.check_pool()
+
+
+def test_runs_out_of_range_do_not_grow_their_sequences():
+    p = Pair((4, 1, 2, 64, 64), 16, [64] * 4, [3, 60, 5, 64], 27)
+    k, v, _ = p.rows(10)
+    cu = torch.tensor([0, 2, 40, 42, 10], dtype=torch.int32, device="cuda")
+    grown = torch.zeros(4, dtype=torch.int32, device="cuda")
+    p.cache.append(k.cuda(), v.cuda(), cu_new=cu, lens_out=grown)
+    assert p.cache.error() == _lib.SAGA_ERR_BOUNDS
+    assert grown.tolist() == [5, 60, 5, 64]
+
+
+@pytest.mark.parametrize("layout,P", [((32, 4, 8, 64, 64), 64), ((12, 2, 2, 128, 128), 16), ((16, 1, 1, 64, 64), 32)])
+def test_decode_scales_that_grow_and_vanish(layout, P):
+    """Logits that rise from position to position (a new reference again and again), value scales from
+    2^-40 to 2^40 in both orders, rows of scale zero (keys, values, the first ones of a sequence)."""
+    hq, hk, hv, dk, dv = layout
+    lens = [40 * 64, 700, 65, 3]
+    p = filled(layout, P, lens, 28)
+    s = p.state
+    for b, n in enumerate(lens):
+        pos = np.arange(n)
+        up = 2.0 ** ((pos * 80) // max(1, n) - 40)
+        for name, d, heads in (("k_pages", dk, hk), ("v_pages", dv, hv)):
+            for h in range(heads):
+                if name == "k_pages":
+                    scale = ref.bf16(0.05 + 0.5 * pos / n) if b != 1 else ref.bf16(0.4 + 0 * pos)
+                else:
+                    scale = (up if b % 2 == 0 else up[::-1]).copy()
+                scale[pos % 7 == 3] = 0.0
+                scale[:min(2, n - 1)] = 0.0
+                raw = torch.from_numpy(np.ascontiguousarray(scale)).bfloat16().view(torch.uint8).numpy().reshape(n, 2)
+                for i in range(n):
+                    block = s[name][s["page_table"][b, i // P], h]
+                    at = P * d // 2 + 2 * (i % P)
+                    block[at:at + 2] = raw[i]
+    p.cache.k_pages.copy_(torch.from_numpy(s["k_pages"]))
+    p.cache.v_pages.copy_(torch.from_numpy(s["v_pages"]))
+    p.check_decode(p.query())
+    q = p.query()
+    q[:] = q[:1, :1].abs()  # the same sign everywhere: large logits
+    p.check_decode((8 * q.float()).bfloat16())
