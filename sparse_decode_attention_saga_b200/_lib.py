@@ -249,35 +249,50 @@ def _row_stride(t) -> int:
     return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
 
 
+# (These take tensors, not addresses, and unpack them in place: a small call costs the host more than the GPU.)
+
 def paged_append(d, n_tokens: int, cu_new, seq_lens, page_table, k_new, v_new, q_new, rope, k_pages, v_pages,
                  bounds, q_out, lens_out, ws, stream=None) -> None:
     """rope: a SagaRope, or None.  New rows [n_tokens, heads, dim] may be a stride apart."""
-    _check("saga_paged_append", load().saga_paged_append(
-        ctypes.byref(d), int(n_tokens), _ptr(cu_new), _ptr(seq_lens), _ptr(page_table), _ptr(k_new),
-        _row_stride(k_new), _ptr(v_new), _row_stride(v_new), _ptr(q_new), 0 if q_new is None else _row_stride(q_new),
-        None if rope is None else ctypes.byref(rope), _ptr(k_pages), _ptr(v_pages), _ptr(bounds), _ptr(q_out),
-        _ptr(lens_out), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+    st = load().saga_paged_append(
+        ctypes.byref(d), n_tokens, None if cu_new is None else cu_new.data_ptr(), seq_lens.data_ptr(),
+        page_table.data_ptr(), k_new.data_ptr(), _row_stride(k_new), v_new.data_ptr(), _row_stride(v_new),
+        None if q_new is None else q_new.data_ptr(), 0 if q_new is None else _row_stride(q_new),
+        None if rope is None else ctypes.byref(rope), k_pages.data_ptr(), v_pages.data_ptr(),
+        None if bounds is None else bounds.data_ptr(), None if q_out is None else q_out.data_ptr(),
+        None if lens_out is None else lens_out.data_ptr(), ws.data_ptr(), ws.nbytes, _stream(stream))
+    if st:
+        _check("saga_paged_append", st)
 
 
 def paged_read(d, n_tokens: int, cu, start, page_table, k_pages, v_pages, k_out, v_out, ws, stream=None) -> None:
-    _check("saga_paged_read", load().saga_paged_read(
-        ctypes.byref(d), int(n_tokens), _ptr(cu), _ptr(start), _ptr(page_table), _ptr(k_pages), _ptr(v_pages),
-        _ptr(k_out), _ptr(v_out), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+    st = load().saga_paged_read(
+        ctypes.byref(d), n_tokens, None if cu is None else cu.data_ptr(), start.data_ptr(), page_table.data_ptr(),
+        k_pages.data_ptr(), v_pages.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), ws.data_ptr(), ws.nbytes,
+        _stream(stream))
+    if st:
+        _check("saga_paged_read", st)
 
 
 def paged_select(d, n_sel: int, n_first: int, n_last: int, q, bounds, seq_lens, page_table, sel_pages, sel_cnt, ws,
                  stream=None) -> None:
-    _check("saga_paged_select", load().saga_paged_select(
-        ctypes.byref(d), int(n_sel), int(n_first), int(n_last), _ptr(q), _ptr(bounds), _ptr(seq_lens),
-        _ptr(page_table), _ptr(sel_pages), _ptr(sel_cnt), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+    st = load().saga_paged_select(
+        ctypes.byref(d), n_sel, n_first, n_last, q.data_ptr(), bounds.data_ptr(), seq_lens.data_ptr(),
+        page_table.data_ptr(), sel_pages.data_ptr(), sel_cnt.data_ptr(), ws.data_ptr(), ws.nbytes, _stream(stream))
+    if st:
+        _check("saga_paged_select", st)
 
 
 def paged_decode(d, q, k_pages, v_pages, seq_lens, page_table, sel_pages, sel_cnt, n_sel: int, out, ws,
                  stream=None) -> None:
     """sel_pages, sel_cnt: the lists of paged_select, or None for every page."""
-    _check("saga_paged_decode", load().saga_paged_decode(
-        ctypes.byref(d), _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(seq_lens), _ptr(page_table), _ptr(sel_pages),
-        _ptr(sel_cnt), int(n_sel), _ptr(out), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+    st = load().saga_paged_decode(
+        ctypes.byref(d), q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), seq_lens.data_ptr(),
+        page_table.data_ptr(), None if sel_pages is None else sel_pages.data_ptr(),
+        None if sel_cnt is None else sel_cnt.data_ptr(), n_sel, out.data_ptr(), ws.data_ptr(), ws.nbytes,
+        _stream(stream))
+    if st:
+        _check("saga_paged_decode", st)
 
 
 def selftest_wait_timeout(ws, limit_us: int, stream=None) -> None:

@@ -28,11 +28,7 @@ namespace saga {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
-constexpr int kChunk = kWarps * 16;  // pages scored by a CTA
-constexpr int kPer = 16;             // pages a thread holds in registers
-constexpr int kRound = kThreads * kPer;
+constexpr int kPer = 16;     // pages a thread holds in registers
 constexpr int kBand = 1024;  // pages scored again in shared memory
 constexpr int kBins = 2048;
 constexpr int kFewInBin = 24;  // pages in the threshold's bin that need no finer histogram
@@ -48,6 +44,7 @@ __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t u) { return *reinter
 __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
 // Sum over the block (two buffers in turn: one barrier a call).
+template <int kWarps>
 __device__ __forceinline__ int block_sum(int n, uint32_t (&buf)[2][kWarps], int& turn) {
     n = __reduce_add_sync(kFull, n);
     if ((threadIdx.x & 31) == 0) buf[turn][threadIdx.x >> 5] = n;
@@ -60,6 +57,7 @@ __device__ __forceinline__ int block_sum(int n, uint32_t (&buf)[2][kWarps], int&
 }
 
 // Exclusive prefix of n over the block's threads, and the total.
+template <int kWarps>
 __device__ __forceinline__ int block_prefix(int n, int& total, uint32_t (&buf)[2][kWarps], int& turn) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int incl = n;
@@ -83,6 +81,7 @@ __device__ __forceinline__ int block_prefix(int n, int& total, uint32_t (&buf)[2
 }
 
 // The largest of v over the block (min: negate).
+template <int kWarps>
 __device__ __forceinline__ float block_max(float v, uint32_t (&buf)[2][kWarps], int& turn) {
     v = warp_max(v);
     if ((threadIdx.x & 31) == 0) buf[turn][threadIdx.x >> 5] = __float_as_uint(v);
@@ -93,9 +92,10 @@ __device__ __forceinline__ float block_max(float v, uint32_t (&buf)[2][kWarps], 
     return v;
 }
 
-template <int DK, int NT>
-__global__ void __launch_bounds__(kThreads, 1) select_kernel(const PagedSelectArgs a, const int groups) {
+template <int DK, int NT, int kThreads>
+__global__ void __launch_bounds__(kThreads, 512 / kThreads) select_kernel(const PagedSelectArgs a, const int groups) {
     constexpr int CH = DK / 32;  // 16-byte chunks of a bound row per lane
+    constexpr int kWarps = kThreads / 32, kChunk = kWarps * 16, kRound = kThreads * kPer;  // kChunk: pages a CTA scores at once
     extern __shared__ uint32_t words[];  // the picked pages' bits, then each word's rank
     __shared__ uint32_t sums[2][kWarps];
     __shared__ uint32_t bins[kBins];
@@ -415,25 +415,33 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const PagedSelectAr
     }
 }
 
-}  // namespace
-
-cudaError_t launch_paged_select(const PagedSelectArgs& a, int sms, cudaStream_t stream) {
+template <int kThreads>
+cudaError_t launch(const PagedSelectArgs& a, int ctas, cudaStream_t stream) {
     const PagedGeom& g = a.g;
     // 16-page groups per warp: one wave of CTAs where the batch needs no more
+    constexpr int kChunk = kThreads / 2;
     const int rows = g.b * g.hk, chunks = (g.max_pages + kChunk - 1) / kChunk;
-    int groups = static_cast<int>((static_cast<long long>(chunks) * rows + sms - 1) / sms);
+    int groups = static_cast<int>((static_cast<long long>(chunks) * rows + ctas - 1) / ctas);
     groups = groups < 1 ? 1 : groups > 4 ? 4 : groups;
     const dim3 grid((chunks + groups - 1) / groups, rows);
-    auto kern = g.Gk <= 8 ? (g.dk == 128  ? select_kernel<128, 1>
-                             : g.dk == 64 ? select_kernel<64, 1>
-                                          : select_kernel<32, 1>)
-                          : (g.dk == 128  ? select_kernel<128, 2>
-                             : g.dk == 64 ? select_kernel<64, 2>
-                                          : select_kernel<32, 2>);
+    auto kern = g.Gk <= 8 ? (g.dk == 128  ? select_kernel<128, 1, kThreads>
+                             : g.dk == 64 ? select_kernel<64, 1, kThreads>
+                                          : select_kernel<32, 1, kThreads>)
+                          : (g.dk == 128  ? select_kernel<128, 2, kThreads>
+                             : g.dk == 64 ? select_kernel<64, 2, kThreads>
+                                          : select_kernel<32, 2, kThreads>);
     const int smem = (g.max_pages + 31) / 32 * 8;  // at most 64 KB (kPagedMaxSelectPages)
     const cudaError_t e = allow_dynamic_smem(kern, smem);
     if (e != cudaSuccess) return e;
     return launch_dependent(kern, grid, dim3(kThreads), smem, stream, a, groups);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_select(const PagedSelectArgs& a, int sms, cudaStream_t stream) {
+    // More rows than SMs: their last CTAs' chains queue up, so smaller CTAs, two or three to an SM (1600 rows of
+    // 157 pages 88 -> 51 us, 240 rows of 625 24.2 -> 21.5, with 64 rows of 2048 17.6 -> 19.6).
+    return a.g.b * a.g.hk > sms ? launch<256>(a, 2 * sms, stream) : launch<512>(a, sms, stream);
 }
 
 }  // namespace saga

@@ -27,15 +27,17 @@ def block_bytes(page_size: int, dim: int) -> int:
 
 def _need(name, t, dtype, shape, device, rows=False):
     """rows: only the dims after the first have to be contiguous (rows a stride apart)."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}, got "
                          f"{f'{t.dtype} {tuple(t.shape)}' if isinstance(t, torch.Tensor) else type(t).__name__}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the cache on {device}")
-    if not t.is_contiguous():
-        if not rows or not t[0].is_contiguous() or t.stride(0) < t[0].numel() or t.stride(0) % 8:
-            raise ValueError(f"{name} must be contiguous" + (" in each row, rows a multiple of 8 elements apart"
-                                                             if rows else ""))
+    step, head, one = t.stride() if t.dim() == 3 else (0, 0, 0)
+    if not rows or one != 1 or head != shape[2] or step < shape[1] * shape[2] or step % 8:
+        raise ValueError(f"{name} must be contiguous" + (" in each row, rows a multiple of 8 elements apart"
+                                                         if rows else ""))
 
 
 class PagedCache:
@@ -57,6 +59,7 @@ class PagedCache:
         if device.type == "cuda" and device.index is None:
             device = torch.device("cuda", torch.cuda.current_device())
         self.device = device
+        self._elsewhere = device.type == "cuda" and torch.cuda.device_count() > 1  # may not be the current device
 
         def buffer(name, t, dtype, shape, fill=None):
             if t is None:
@@ -81,8 +84,8 @@ class PagedCache:
         self.ws = torch.zeros(nbytes, dtype=u8, device=device)
 
     def _on(self, stream):
-        """The stream to enqueue on: the given one, or the cache's device's current one."""
-        return torch.cuda.current_stream(self.device) if stream is None else stream
+        """The stream to enqueue on: the given one, or the cache's device's current one (its handle)."""
+        return torch._C._cuda_getCurrentRawStream(self.device.index) if stream is None else stream
 
     def _new(self, shape, dtype, stream, zero=False):
         """A tensor made on the stream that the call runs on."""
@@ -95,7 +98,7 @@ class PagedCache:
             return make(shape, dtype=dtype, device=self.device)
 
     def _call(self, fn, *args, stream):
-        if self.device.type == "cuda" and self.device.index != torch.cuda.current_device():
+        if self._elsewhere and self.device.index != torch.cuda.current_device():
             with torch.cuda.device(self.device):
                 fn(*args, self._on(stream))
         else:
@@ -218,7 +221,7 @@ class PagedCache:
 
     def error(self, stream=None) -> int:
         """The sticky device flag (read and cleared; synchronises the stream)."""
-        if self.device.type == "cuda" and self.device.index != torch.cuda.current_device():
+        if self._elsewhere and self.device.index != torch.cuda.current_device():
             with torch.cuda.device(self.device):
                 return _lib.workspace_error(self.ws, self._on(stream))
         return _lib.workspace_error(self.ws, self._on(stream))
