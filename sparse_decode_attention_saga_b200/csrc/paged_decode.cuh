@@ -32,6 +32,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "paged.h"
 #include "saga_device.cuh"
 
@@ -53,6 +55,9 @@ constexpr int kRound = 4;  // tiles between two arrivals at the pace barrier
 // largest scale: room for a logit to pass the accumulators' reference before a
 // new one is taken, when a product reaches 2^15.
 constexpr int kUnit = 8;
+// Biased exponent that the largest scale is taken for at least (2^-67): exponentials
+// in that unit and their sums stay far from fp32's end.
+constexpr int kLeastExpo = 60;
 // The reference before a row's first position: its product overflows and brings one.
 constexpr float kNone = -1e30f;
 // log2(e) / sqrt(d): logits count in powers of two
@@ -83,6 +88,14 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Two 16x16 byte matrices (lanes 0-15 and 16-31 give the rows' addresses):
+// register 2i + j gets bytes (rows 4 (lane % 4) .. + 3, column lane / 4 + 8 j) of matrix i.
+__device__ __forceinline__ void load_columns(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -245,6 +258,7 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
     const int n_my = static_cast<int>(w1 - w0);
 
     uint8_t* my_ring = ring + static_cast<size_t>(warp) * stages * S::stage_bytes;
+    constexpr uint32_t kAllValid = EPT == 1 ? P : EPT == 2 ? P * 0x0101u : P * 0x01010101u;  // a byte per page
     constexpr int k_bytes = EPT * KBLK;
     constexpr uint32_t v_bytes = NVU * VBLK;
 
@@ -342,9 +356,12 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
     int row = -1, seen = 0, expo = 0;  // seen: flags of the row's tiles so far; expo: biased exponent of the largest scale
     uint32_t qf[NT][KS][2];
     float c0[NT][2], colf[NT][2], m[NT][2], l[NT][2];
-    float unit = 0.f;  // factor of the scales, 2^(kUnit - their largest exponent)
+    float base[NT][2];  // the reference less the unit: exponentials are in units of 2^-kUnit of the largest scale
     float acc[ACC][MT][4];
-    const int pos_a = (gq >> 1) + 4 * (gq & 1);  // position (of 16) of tile row gq; row gq + 8: 8 more
+    // Rows gq and gq + 8 of a key tile are positions 2 gq and 2 gq + 1 (of 16): after the transposition a lane
+    // then has the probabilities of positions 4 tq, 4 tq + 2 and 4 tq + 1, 4 tq + 3, as it has the values.
+    const int pos_a = 2 * gq;
+    const uint32_t v_lane_row = (lane & 15) * (DV / 2) + (lane >> 4) * 16;  // its address for load_columns
 
     // query head (of the work row) in column c of tile nt, or -1
     auto head_of = [&](int nt, int c) {
@@ -355,8 +372,7 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
     auto begin_row = [&](int r) {
         row = r;
         seen = 0;
-        expo = 20;
-        unit = pow2i(kUnit + 127 - 20);
+        expo = kLeastExpo;
         const int vg = r % nvg, bk = r / nvg;  // bk = b * hk + kh
         const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) +
                                  (static_cast<size_t>(bk) * g.nvk + vg * NVU) * g.Gv * DK;
@@ -406,6 +422,7 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
                 c0[nt][i] = __shfl_sync(kFull, start, (2 * tq + i) * 4);
                 colf[nt][i] = __shfl_sync(kFull, f, (2 * tq + i) * 4);
                 m[nt][i] = kNone;
+                base[nt][i] = kNone;
                 l[nt][i] = 0.f;
             }
         }
@@ -426,7 +443,7 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
     };
     // The values of o that this lane has, NV of them: for CW 4 the sums of the
     // two halves (columns c and c + 4 of a tile are one head; the left lanes
-    // add them up for dims 8 gq + 2 k, the right ones for 8 gq + 2 k + 1).
+    // add them up for the even dims, the right ones for the odd).
     // Value k belongs to head (of the work row's columns) lane_head + head_at(k)
     // and dim lane_dim + dim_at(k).
     auto fragment = [&](int k) {
@@ -443,10 +460,10 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
     auto frag_head = [](int k) { return CW == 4 ? 4 * (k / (2 * MT)) + k % 2 : 8 * (k / (4 * MT)) + k % 2; };
     auto frag_dim = [](int k) {
         const int mt = CW == 4 ? k / 2 % MT : k / 4 % MT;
-        return 64 * (mt >> 2) + 2 * (mt & 3) + (CW == 4 ? 0 : k / 2 % 2);
+        return 16 * mt + (CW == 4 ? 0 : k / 2 % 2);
     };
     auto lane_head = [](int ln) { return CW == 4 ? 2 * (ln & 1) : 2 * (ln & 3); };
-    auto lane_dim = [](int ln) { return 8 * (ln >> 2) + (CW == 4 ? (ln >> 1) & 1 : 0); };
+    auto lane_dim = [](int ln) { return 2 * (ln >> 2) + (CW == 4 ? (ln >> 1) & 1 : 0); };
     // a column's place among the row's heads in the output, or -1
     auto out_head = [&](int c) { return c % CW < g.Gv ? c / CW * g.Gv + c % CW : -1; };
     auto row_out = [&](int r) { return a.out + (static_cast<size_t>(r / nvg) * g.nvk + r % nvg * NVU) * g.Gv * DV; };
@@ -465,7 +482,7 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) f[nt][i] = !whole ? scale_unit : l[nt][i] > 0.f ? scale_unit * __fdividef(1.f, l[nt][i]) : 0.f;
+            for (int i = 0; i < 2; ++i) f[nt][i] = !whole ? scale_unit : l[nt][i] > 0.f ? __fdividef(1.f, l[nt][i]) : 0.f;
         // an end of the range stays in this warp's ring (its copies are all in), an earlier piece goes to the workspace
         float* dst = end_of_range ? reinterpret_cast<float*>(my_ring)
                                   : a.firsts + (static_cast<size_t>(blockIdx.x) * kWarps + warp) * kRecord;
@@ -475,7 +492,7 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     if (8 * nt + 2 * tq + i < kColumns)
-                        reinterpret_cast<float2*>(dst)[8 * nt + 2 * tq + i] = make_float2(m[nt][i], l[nt][i]);
+                        reinterpret_cast<float2*>(dst)[8 * nt + 2 * tq + i] = make_float2(m[nt][i], l[nt][i] * scale_unit);
         }
         float* to = row_out(row) + lane_dim(lane);
         float fx[ACC][2];
@@ -516,7 +533,7 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
     const int v_lane = CW == 4 ? min(tq >> 1, NVU - 1) * VBLK : 0;
 
     // ---- 16 positions: group gi of the stage's tile
-    auto consume = [&](const uint8_t* buf, uint32_t tile_valid, uint32_t gi) {
+    auto consume = [&](const uint8_t* buf, uint32_t tile_valid, uint32_t gi, auto all_valid) {
         const uint32_t e = gi * 16 / P, in = gi * 16 % P;  // the group's page and its place in it
         const int valid = static_cast<int>((tile_valid >> (8 * e)) & 0xffu) - static_cast<int>(in);
         const uint8_t* kb = buf + e * KBLK;
@@ -525,7 +542,7 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
         uint32_t w[2][WK];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            const uint8_t* src = krow + r * 8 * (DK / 2);
+            const uint8_t* src = krow + r * (DK / 2);
             if constexpr (WK == 1) {
                 w[r][0] = *reinterpret_cast<const uint32_t*>(src);
             } else if constexpr (WK == 2) {
@@ -536,16 +553,12 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
                 w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
             }
         }
-        const uint16_t* ks = reinterpret_cast<const uint16_t*>(kb + P * (DK / 2)) + in + pos_a;
-        uint32_t kscale[2], vscale[NT][2];
+        // the scales of the two positions, the first in the low half
+        uint32_t kscale = *reinterpret_cast<const uint32_t*>(kb + P * (DK / 2) + 2 * (in + pos_a)), vscale[NT];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            kscale[r] = ks[8 * r];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int j = CW == 4 ? 2 * nt : CW == 8 ? nt : 0;
-                vscale[nt][r] = reinterpret_cast<const uint16_t*>(vb + j * VBLK + v_lane + P * (DV / 2))[in + pos_a + 8 * r];
-            }
+        for (int nt = 0; nt < NT; ++nt) {
+            const int j = CW == 4 ? 2 * nt : CW == 8 ? nt : 0;
+            vscale[nt] = *reinterpret_cast<const uint32_t*>(vb + j * VBLK + v_lane + P * (DV / 2) + 2 * (in + pos_a));
         }
         float x[NT][4];
 #pragma unroll
@@ -560,25 +573,23 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
             }
         }
         float off[2] = {0.f, 0.f};  // -inf at the positions past the end, whose scales count as 0
-        if (valid < 16) {
+        if (!decltype(all_valid)::value && valid < 16) {
+            const uint32_t keep = pos_a + 1 < valid ? 0xffffffffu : pos_a < valid ? 0x0000ffffu : 0u;
+            off[0] = pos_a < valid ? 0.f : -kInf;
+            off[1] = pos_a + 1 < valid ? 0.f : -kInf;
+            kscale &= keep;
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
-                if (pos_a + 8 * r >= valid) {
-                    off[r] = -kInf;
-                    kscale[r] = 0;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) vscale[nt][r] = 0;
-                }
+            for (int nt = 0; nt < NT; ++nt) vscale[nt] &= keep;
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const float s = __uint_as_float(kscale[r] << 16);
+                const float s = r ? bf16_hi(kscale) : bf16_lo(kscale);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) x[nt][2 * r + i] = __fmaf_rn(x[nt][2 * r + i], colf[nt][i] * s, off[r]);
+                for (int i = 0; i < 2; ++i) x[nt][2 * r + i] = __fmaf_rn(x[nt][2 * r + i], s, off[r]);
             }
-        // p = 2^(x - reference), y = p times its row's scale, in two fp16 halves
+        // p = 2^(logit - reference + unit), y = p times its row's scale, in two fp16 halves
         float p[NT][4], y[NT][4];
         uint32_t hi[NT][2], lo[NT][2];
         auto products = [&]() {
@@ -587,10 +598,10 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const float s = __uint_as_float(vscale[nt][r] << 16) * unit;
+                    const float s = r ? bf16_hi(vscale[nt]) : bf16_lo(vscale[nt]);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        p[nt][2 * r + i] = exp2_approx(x[nt][2 * r + i] - m[nt][i]);
+                        p[nt][2 * r + i] = exp2_approx(__fmaf_rn(x[nt][2 * r + i], colf[nt][i], -base[nt][i]));
                         y[nt][2 * r + i] = p[nt][2 * r + i] * s;
                     }
                     const __half2 h = __floats2half2_rn(y[nt][2 * r], y[nt][2 * r + 1]);
@@ -604,26 +615,28 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
             float f[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                top = max(top, max(vscale[nt][0] & 0x7fffu, vscale[nt][1] & 0x7fffu));
+                top = max(top, max(vscale[nt] & 0x7fffu, (vscale[nt] >> 16) & 0x7fffu));
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     float v = fmaxf(x[nt][i], x[nt][2 + i]);
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
-                    v = fmaxf(v, m[nt][i]);
+                    v = fmaxf(v * colf[nt][i], m[nt][i]);
                     f[nt][i] = exp2_approx(m[nt][i] - v);
-                    l[nt][i] = f[nt][i] > 0.f ? l[nt][i] * f[nt][i] : 0.f;
                     m[nt][i] = v;
                 }
             }
             const int en = max(expo, static_cast<int>(__reduce_max_sync(kFull, top) >> 7));
             const float shift = en - expo < 126 ? pow2i(expo - en) : 0.f;
             expo = en;
-            unit = pow2i(kUnit + 127 - en);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) f[nt][i] *= shift;
+                for (int i = 0; i < 2; ++i) {
+                    base[nt][i] = m[nt][i] - static_cast<float>(kUnit + 127 - en);
+                    f[nt][i] *= shift;
+                    l[nt][i] = f[nt][i] > 0.f ? l[nt][i] * f[nt][i] : 0.f;
+                }
 #pragma unroll
             for (int xx = 0; xx < ACC; ++xx) {
                 float fx[2];
@@ -666,21 +679,17 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
         for (int j = 0; j < NVU; ++j) {
 #pragma unroll
             for (int half = 0; half < DV / 64; ++half) {
-                // word gq (+ 8) of rows tq, tq + 4, tq + 8, tq + 12
-                const uint32_t* row0 = reinterpret_cast<const uint32_t*>(vb + j * VBLK + (in + tq) * (DV / 2)) + gq + 8 * half;
-                const uint32_t u0 = row0[0], u1 = row0[4 * DV / 8], u2 = row0[8 * DV / 8], u3 = row0[12 * DV / 8];
+                uint32_t u[4];
+                load_columns(smem_addr(vb + j * VBLK + in * (DV / 2)) + v_lane_row + 32 * half, u);
+                {
 #pragma unroll
-                for (int part_ = 0; part_ < 2; ++part_) {  // nibbles 0-3, 4-7 of the words
-                    const uint32_t sel = part_ ? 0x7632u : 0x5410u;
-                    const uint32_t a_ = __byte_perm(u0, u1, sel), b_ = __byte_perm(u2, u3, sel);
-#pragma unroll
-                    for (int by = 0; by < 2; ++by) {
-                        const uint32_t av = by ? a_ >> 8 : a_, bv = by ? b_ >> 8 : b_;
-                        const uint32_t f0 = half2_bits(__hsub2(bits_half2(and_or<0x000f000fu>(av, k1024)), k1032));
-                        const uint32_t f1 = half2_bits(__hfma2(bits_half2(and_or<0x00f000f0u>(av, k1024)), k16th, k72));
-                        const uint32_t f2 = half2_bits(__hsub2(bits_half2(and_or<0x000f000fu>(bv, k1024)), k1032));
-                        const uint32_t f3 = half2_bits(__hfma2(bits_half2(and_or<0x00f000f0u>(bv, k1024)), k16th, k72));
-                        const int mt = 4 * half + 2 * part_ + by;
+                    for (int i = 0; i < 4; ++i) {  // 16 dims: the bytes' low numbers are row gq, the high ones row gq + 8
+                        const uint32_t odd = u[i] >> 8;
+                        const uint32_t f0 = half2_bits(__hsub2(bits_half2(and_or<0x000f000fu>(u[i], k1024)), k1032));
+                        const uint32_t f1 = half2_bits(__hfma2(bits_half2(and_or<0x00f000f0u>(u[i], k1024)), k16th, k72));
+                        const uint32_t f2 = half2_bits(__hsub2(bits_half2(and_or<0x000f000fu>(odd, k1024)), k1032));
+                        const uint32_t f3 = half2_bits(__hfma2(bits_half2(and_or<0x00f000f0u>(odd, k1024)), k16th, k72));
+                        const int mt = 4 * half + i;
                         if constexpr (CW == 4) {
                             mma_f16(acc[j][mt], f0, f1, f2, f3, ph[j][0], ph[j][1]);
                         } else if constexpr (CW == 8) {
@@ -728,8 +737,13 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
         if (done == n_my) break;  // (a warp without a tile)
         seen |= (meta.y == 0 ? 1 : 0) | (meta.y == tiles - 1 ? 2 : 0);
         const uint8_t* buf = my_ring + s * S::stage_bytes;
+        if (static_cast<uint32_t>(meta.w) == kAllValid) {
 #pragma unroll
-        for (uint32_t gi = 0; gi < kTile / 16; ++gi) consume(buf, meta.w, gi);
+            for (uint32_t gi = 0; gi < kTile / 16; ++gi) consume(buf, meta.w, gi, std::true_type{});
+        } else {
+#pragma unroll 1
+            for (uint32_t gi = 0; gi < kTile / 16; ++gi) consume(buf, meta.w, gi, std::false_type{});
+        }
         __syncwarp();
         if (produced < n_my) {
             produce(s);
