@@ -26,7 +26,7 @@
 #include <cuda_bf16.h>
 
 #include "paged.h"
-#include "saga_device.cuh"
+#include "paged_device.cuh"
 
 namespace saga {
 

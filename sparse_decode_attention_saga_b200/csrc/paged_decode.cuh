@@ -48,7 +48,7 @@
 #include <type_traits>
 
 #include "paged.h"
-#include "saga_device.cuh"
+#include "paged_device.cuh"
 
 namespace saga {
 
