@@ -21,8 +21,8 @@
 // bound leaves its bf16 rounding open (one value in some 2000); a quotient is
 // a product with the scale's reciprocal, put on a grid of 2^-12 (halves stay
 // halves, and no other quotient is within 2^-11 of one).  Measured, with the read
-// of the written rows: 20.7K tokens of 32/4/8 heads of 64 in 12 runs 69 us (248 MB,
-// 0.55 of the copy rate; 73 % of the issue slots), 256 single tokens 9.4 us.
+// of the written rows: 20.7K tokens of 32/4/8 heads of 64 in 12 runs 66 us (248 MB,
+// 0.58 of the copy rate; 73 % of the issue slots), 256 single tokens 7.3 us.
 #include <cuda_bf16.h>
 
 #include "paged.h"
@@ -35,7 +35,7 @@ namespace {
 // Small CTAs, many to an SM: a unit's start is a chain of dependent loads (run,
 // length, page) that only other CTAs hide.
 constexpr int kThreads = 128;
-constexpr int kResident = 6;
+constexpr int kResident = 5;
 constexpr int kDepth = 4;        // rows of a lane in flight
 constexpr int kPartsPerSm = 12;  // CTAs per SM that a launch aims for by splitting the heads of its units
 constexpr uint32_t kFull = 0xffffffffu;
@@ -48,58 +48,63 @@ struct Unit {
 
 // Units of sequence i start at cu[i]/P + 2i: a run of n tokens touches at
 // most n/P + 2 pages, so that the ranges do not overlap.
-__device__ __forceinline__ int unit_start(const int32_t* cu, int i, int P) { return max(cu[i], 0) / P + 2 * i; }
+__device__ __forceinline__ int unit_start(int cu, int i, int shift) { return (max(cu, 0) >> shift) + 2 * i; }
 
+// (w.phys is the table's entry as it is, still on its way: has_page checks it.)
 __device__ __forceinline__ bool find_unit(const PagedAppendArgs& a, int u, Unit& w) {
     const PagedGeom& g = a.g;
-    const int lane = threadIdx.x & 31;
-    int seq, j, n, t0;
+    const int lane = threadIdx.x & 31, shift = 31 - __clz(g.P);
+    int seq, j, n, t0, len0;
     if (!a.cu) {
         if (u >= g.b) return false;
         seq = u, j = 0, n = 1, t0 = u;
+        len0 = a.seq_lens[seq];
     } else {
         int lo = 0, len = g.b;
-        while (true) {  // 32-ary search for the last sequence that starts at or before u
+        // 32-ary search for the last sequence that starts at or before u; the last level's lanes bring all that
+        // is needed of theirs
+        while (len > 32) {
             const int step = (len + 31) / 32;
-            const bool in = lane * step < len && unit_start(a.cu, lo + lane * step, g.P) <= u;
-            const int c = __popc(__ballot_sync(0xffffffffu, in));
+            const bool in = lane * step < len && unit_start(a.cu[lo + lane * step], lo + lane * step, shift) <= u;
+            const int c = __popc(__ballot_sync(kFull, in));
             if (c == 0) return false;
             lo += (c - 1) * step;
             len = min(step, len - (c - 1) * step);
-            if (step == 1) break;
         }
-        seq = lo;
-        t0 = a.cu[seq];
-        n = a.cu[seq + 1] - t0;
-        j = u - unit_start(a.cu, seq, g.P);
+        const int i = lo + min(lane, len - 1);
+        const int c0 = a.cu[i], c1 = a.cu[i + 1], start = unit_start(c0, i, shift), l0 = a.seq_lens[i];
+        const int c = __popc(__ballot_sync(kFull, lane < len && start <= u));
+        if (c == 0) return false;
+        seq = lo + c - 1;
+        t0 = __shfl_sync(kFull, c0, c - 1);
+        n = __shfl_sync(kFull, c1, c - 1) - t0;
+        j = u - __shfl_sync(kFull, start, c - 1);
+        len0 = __shfl_sync(kFull, l0, c - 1);
         if (t0 < 0 || n < 0 || t0 > a.n_tokens - n) {
             if (threadIdx.x == 0) raise_device_error(a.err, kErrBounds);
             return false;
         }
     }
     if (n == 0) return false;
-    const int len0 = a.seq_lens[seq];
     if (len0 < 0 || len0 > g.max_pages * g.P) {
         if (threadIdx.x == 0) raise_device_error(a.err, kErrBounds);
         return false;
     }
-    const int page = len0 / g.P + j;
+    const int page = (len0 >> shift) + j;
     const int first = max(len0, page * g.P), last = min(len0 + n, (page + 1) * g.P);
     if (first >= last) return false;
-    const int phys = page < g.max_pages ? a.page_table[static_cast<size_t>(seq) * g.max_pages + page] : -1;
-    if (phys < 0 || phys >= g.n_pages) {  // no such page: its rows are not written
-        if (threadIdx.x == 0) raise_device_error(a.err, kErrBounds);
-        return false;
-    }
+    w.phys = page < g.max_pages ? a.page_table[static_cast<size_t>(seq) * g.max_pages + page] : -1;
     w.seq = seq;
     w.page = page;
     w.off = first - page * g.P;
     w.rows = last - first;
     w.token = t0 + (first - len0);
-    w.phys = phys;
     w.old_rows = len0 > page * g.P;
     return true;
 }
+
+// Whether the unit's page is in the pool; its rows are left alone otherwise.
+__device__ __forceinline__ bool has_page(const PagedAppendArgs& a, const Unit& w) { return w.phys >= 0 && w.phys < a.g.n_pages; }
 
 // x1 a + x2 b rounded once to fp32 (products and sum split into value and error).
 __device__ __forceinline__ float dot2_rn(float x1, float a, float x2, float b) {
@@ -279,6 +284,7 @@ __device__ __forceinline__ void write_rows(const PagedAppendArgs& a, const Unit&
         };
 #pragma unroll
         for (int i = 0; i < kDepth; ++i) issue(i, i * sp.hp);
+        if (!has_page(a, w)) break;  // (looked at once the rows are on their way)
         int slot = 0;
         for (int at = 0; at < total; at += sp.hp) {  // every warp of the CTA the same number of times
             cp_async_wait<kDepth - 1>();
@@ -312,7 +318,26 @@ __device__ __forceinline__ void write_rows(const PagedAppendArgs& a, const Unit&
                     if (threadIdx.x % LPR == 0) *reinterpret_cast<__nv_bfloat16*>(to + scale_at) = scale;
                 }
             }
-            if (a.bounds && at < n.nk) {  // this warp's rows of each key head, then the CTA's
+            if (a.bounds && at < n.nk && w.rows == 1) {  // a single row: straight to the page's bounds
+                if (live && key) {
+                    uint4* box = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.bounds) + (page_row * g.hk + n.k0 + i) * 2 * D);
+                    auto widen = [&](uint4* to, uint4 v, bool up) {
+                        if (w.old_rows) {
+                            const uint4 o = *to;
+                            const uint32_t x[4] = {v.x, v.y, v.z, v.w}, y[4] = {o.x, o.y, o.z, o.w};
+                            uint32_t r[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) r[j] = as_u32(up ? __hmax2(as_bf162(x[j]), as_bf162(y[j])) : __hmin2(as_bf162(x[j]), as_bf162(y[j])));
+                            v = make_uint4(r[0], r[1], r[2], r[3]);
+                        }
+                        *to = v;
+                    };
+                    widen(box + pairs.ca, va, false);
+                    widen(box + pairs.cb, vb, false);
+                    widen(box + D / 8 + pairs.ca, va, true);
+                    widen(box + D / 8 + pairs.cb, vb, true);
+                }
+            } else if (a.bounds && at < n.nk) {  // this warp's rows of each key head, then the CTA's
                 uint32_t lo[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w}, hi[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -342,6 +367,7 @@ __device__ __forceinline__ void write_rows(const PagedAppendArgs& a, const Unit&
         }
         cp_async_wait<0>();
     }
+    cp_async_wait<0>();
 }
 
 // Heads are numbered keys, values, queries; CTA y takes [y*per, (y+1)*per).
@@ -361,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, kResident) append_kernel(const Paged
     if (live) {
         const int h0 = blockIdx.y * per, h1 = min(h0 + per, g.hk + g.hv + (a.q_new ? g.hq : 0));
         const int k1 = min(h1, g.hk);
-        const bool bounds = a.bounds && h0 < k1;
+        const bool bounds = a.bounds && h0 < k1 && w.rows > 1;
         if (bounds) {
             for (int i = threadIdx.x; i < (k1 - h0) * 2 * DK; i += kThreads)
                 (&lo_hi[0][0][0])[i] = (i / DK) & 1 ? 0u : 0xffffffffu;
@@ -376,7 +402,8 @@ __global__ void __launch_bounds__(kThreads, kResident) append_kernel(const Paged
             if (values.nv) write_rows<DV, kNoRotation>(a, w, values, true, nullptr, slots);
         }
         if (n.nk + n.nv + n.nq) write_rows<DK, MODE>(a, w, n, false, lo_hi, slots);
-        if (bounds) {
+        if (!has_page(a, w) && threadIdx.x == 0) raise_device_error(a.err, kErrBounds);
+        if (bounds && has_page(a, w)) {
             __syncthreads();
             __nv_bfloat16* box = reinterpret_cast<__nv_bfloat16*>(a.bounds) +
                                  (static_cast<size_t>(w.phys) * g.hk + h0) * 2 * DK;
@@ -390,17 +417,20 @@ __global__ void __launch_bounds__(kThreads, kResident) append_kernel(const Paged
             }
         }
     }
-    // The grown lengths, once every CTA has read the old ones.
+    // The grown lengths: in place once every CTA has read the old ones, elsewhere at once.
     if (a.lens_out) {
-        __shared__ bool last;
-        __syncthreads();
+        __shared__ bool mine;
+        const bool in_place = a.lens_out == a.seq_lens;
+        if (in_place) __syncthreads();
         if (threadIdx.x == 0) {
-            const unsigned n = gridDim.x * gridDim.y;
-            last = atomicAdd(a.ticket, 1u) == n - 1;
-            if (last) *a.ticket = 0u;
+            mine = blockIdx.x == 0 && blockIdx.y == 0;
+            if (in_place) {
+                mine = atomicAdd(a.ticket, 1u) == gridDim.x * gridDim.y - 1;
+                if (mine) *a.ticket = 0u;
+            }
         }
         __syncthreads();
-        if (last)
+        if (mine)
             for (int i = threadIdx.x; i < g.b; i += kThreads) {
                 const int len = a.seq_lens[i], t0 = a.cu ? a.cu[i] : 0, n = a.cu ? a.cu[i + 1] - t0 : 1;
                 const bool run = t0 >= 0 && n >= 0 && t0 <= a.n_tokens - n && len >= 0;  // else skipped and flagged
@@ -443,6 +473,10 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const PagedAppendArgs a,
     const PagedGeom& g = a.g;
     Unit w;
     if (!find_unit(a, blockIdx.x, w)) return;
+    if (!has_page(a, w)) {
+        if (threadIdx.x == 0) raise_device_error(a.err, kErrBounds);
+        return;
+    }
     const int h0 = blockIdx.y * per, h1 = min(h0 + per, g.hk + g.hv);
     if (h0 < g.hk) read_rows<DK>(a, w, a.k_pages, g.hk, g.kblk, a.k_out, h0, min(h1, g.hk));
     const int v0 = max(h0 - g.hk, 0), v1 = h1 - g.hk;
