@@ -357,7 +357,7 @@ size_t saga_paged_workspace_bytes(const saga_paged_dims* dims);
  *   q_out null: keys and values only.
  *   bounds (nullable): the touched pages' key bounds, set anew where the call
  *   writes a page's first row, else widened.
- *   lens_out (nullable): the grown lengths; may be seq_lens itself.
+ *   lens_out (nullable): the grown lengths; seq_lens itself, or apart from it.
  * A page that the call writes to belongs to one sequence only.  Rows past
  * max_pages * page_size or whose position is not in the rotation table are
  * not written (nor their queries) and set the sticky flag; so is the whole
