@@ -244,20 +244,20 @@ def paged_workspace_bytes(d: SagaPagedDims) -> int:
     return int(load().saga_paged_workspace_bytes(ctypes.byref(d)))
 
 
-def _row_stride(t) -> int:
-    """Elements from one row to the next (of a single row: its own length)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-
-
 # (These take tensors, not addresses, and unpack them in place: a small call costs the host more than the GPU.)
 
 def paged_append(d, n_tokens: int, cu_new, seq_lens, page_table, k_new, v_new, q_new, rope, k_pages, v_pages,
                  bounds, q_out, lens_out, ws, stream=None) -> None:
     """rope: a SagaRope, or None.  New rows [n_tokens, heads, dim] may be a stride apart."""
+    if n_tokens > 1:
+        ks, vs, qs = k_new.stride(0), v_new.stride(0), 0 if q_new is None else q_new.stride(0)
+    else:  # a single row: its own length
+        dv = d.v_head_dim or d.head_dim
+        ks, vs, qs = d.h_k * d.head_dim, d.h_v * dv, 0 if q_new is None else d.h_q * d.head_dim
     st = load().saga_paged_append(
         ctypes.byref(d), n_tokens, None if cu_new is None else cu_new.data_ptr(), seq_lens.data_ptr(),
-        page_table.data_ptr(), k_new.data_ptr(), _row_stride(k_new), v_new.data_ptr(), _row_stride(v_new),
-        None if q_new is None else q_new.data_ptr(), 0 if q_new is None else _row_stride(q_new),
+        page_table.data_ptr(), k_new.data_ptr(), ks, v_new.data_ptr(), vs,
+        None if q_new is None else q_new.data_ptr(), qs,
         None if rope is None else ctypes.byref(rope), k_pages.data_ptr(), v_pages.data_ptr(),
         None if bounds is None else bounds.data_ptr(), None if q_out is None else q_out.data_ptr(),
         None if lens_out is None else lens_out.data_ptr(), ws.data_ptr(), ws.nbytes, _stream(stream))

@@ -27,8 +27,11 @@ def block_bytes(page_size: int, dim: int) -> int:
 
 def _need(name, t, dtype, shape, device, rows=False):
     """rows: only the dims after the first have to be contiguous (rows a stride apart)."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
-        return
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+            return
+    except AttributeError:  # not a tensor
+        pass
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}, got "
                          f"{f'{t.dtype} {tuple(t.shape)}' if isinstance(t, torch.Tensor) else type(t).__name__}")
@@ -82,6 +85,10 @@ class PagedCache:
         elif rot_dim:
             raise ValueError("rot_dim without a rotation table")
         self.ws = torch.zeros(nbytes, dtype=u8, device=device)
+        # (a ctypes field costs as much to read as a check: the shapes once)
+        self._batch = batch
+        self._k_row, self._v_row, self._q_row = (h_k, head_dim), (h_v, self.dv), (h_q, head_dim)
+        self._q, self._out, self._count = (batch, h_q, head_dim), (batch, h_q, self.dv), (batch, h_k)
 
     def _on(self, stream):
         """The stream to enqueue on: the given one, or the cache's device's current one (its handle)."""
@@ -123,52 +130,52 @@ class PagedCache:
         (None: one row each).  Returns the rotated queries (None without
         q_new).  The grown lengths go to seq_lens, or to lens_out if given
         (seq_lens then stays)."""
-        d, dev, bf = self.dims, self.device, torch.bfloat16
+        dev, bf, batch = self.device, torch.bfloat16, self._batch
         T = k_new.shape[0]
-        _need("k_new", k_new, bf, (T, d.h_k, d.head_dim), dev, rows=True)
-        _need("v_new", v_new, bf, (T, d.h_v, self.dv), dev, rows=True)
+        _need("k_new", k_new, bf, (T, *self._k_row), dev, rows=True)
+        _need("v_new", v_new, bf, (T, *self._v_row), dev, rows=True)
         if cu_new is not None:
-            _need("cu_new", cu_new, torch.int32, (d.batch + 1,), dev)
-        elif T != d.batch:
+            _need("cu_new", cu_new, torch.int32, (batch + 1,), dev)
+        elif T != batch:
             raise ValueError("without cu_new there is one new row per sequence")
         if q_new is not None:
-            _need("q_new", q_new, bf, (T, d.h_q, d.head_dim), dev, rows=True)
+            _need("q_new", q_new, bf, (T, *self._q_row), dev, rows=True)
             if q_out is None:
-                q_out = self._new((T, d.h_q, d.head_dim), bf, stream)
+                q_out = self._new((T, *self._q_row), bf, stream)
             else:
-                _need("q_out", q_out, bf, (T, d.h_q, d.head_dim), dev)
+                _need("q_out", q_out, bf, (T, *self._q_row), dev)
         elif q_out is not None:
             raise ValueError("q_out without q_new")
         if lens_out is None:
             lens_out = self.seq_lens
         else:
-            _need("lens_out", lens_out, torch.int32, (d.batch,), dev)
-        self._call(_lib.paged_append, d, T, cu_new, self.seq_lens, self.page_table, k_new, v_new, q_new, self._rope,
+            _need("lens_out", lens_out, torch.int32, (batch,), dev)
+        self._call(_lib.paged_append, self.dims, T, cu_new, self.seq_lens, self.page_table, k_new, v_new, q_new, self._rope,
                    self.k_pages, self.v_pages, self.bounds, q_out, lens_out, self.ws, stream=stream)
         return q_out
 
     def read(self, n_tokens, cu=None, start=None, k_out=None, v_out=None, stream=None):
         """Rows start[b] .. of each sequence (None: from seq_lens, the rows an
         append with lens_out wrote) as bf16 ([T, h_k, d], [T, h_v, d_v])."""
-        d, dev, bf = self.dims, self.device, torch.bfloat16
+        dev, bf, batch = self.device, torch.bfloat16, self._batch
         if cu is not None:
-            _need("cu", cu, torch.int32, (d.batch + 1,), dev)
-        elif n_tokens != d.batch:
+            _need("cu", cu, torch.int32, (batch + 1,), dev)
+        elif n_tokens != batch:
             raise ValueError("without cu one row of each sequence is read")
         if start is None:
             start = self.seq_lens
         else:
-            _need("start", start, torch.int32, (d.batch,), dev)
-        shapes = (n_tokens, d.h_k, d.head_dim), (n_tokens, d.h_v, self.dv)
+            _need("start", start, torch.int32, (batch,), dev)
+        k_shape, v_shape = (n_tokens, *self._k_row), (n_tokens, *self._v_row)
         if k_out is None:
-            k_out = self._new(shapes[0], bf, stream)
+            k_out = self._new(k_shape, bf, stream)
         else:
-            _need("k_out", k_out, bf, shapes[0], dev)
+            _need("k_out", k_out, bf, k_shape, dev)
         if v_out is None:
-            v_out = self._new(shapes[1], bf, stream)
+            v_out = self._new(v_shape, bf, stream)
         else:
-            _need("v_out", v_out, bf, shapes[1], dev)
-        self._call(_lib.paged_read, d, n_tokens, cu, start, self.page_table, self.k_pages, self.v_pages, k_out, v_out,
+            _need("v_out", v_out, bf, v_shape, dev)
+        self._call(_lib.paged_read, self.dims, n_tokens, cu, start, self.page_table, self.k_pages, self.v_pages, k_out, v_out,
                    self.ws, stream=stream)
         return k_out, v_out
 
@@ -176,37 +183,37 @@ class PagedCache:
         """The pages (at most n_sel, [batch, h_k, n_sel] int32, ascending, and
         their number [batch, h_k]) that each key head's queries attend to: the
         first and last ones and those with the largest bounds on their logits."""
-        d, dev, i32 = self.dims, self.device, torch.int32
-        _need("q", q, torch.bfloat16, (d.batch, d.h_q, d.head_dim), dev)
+        dev, i32 = self.device, torch.int32
+        _need("q", q, torch.bfloat16, self._q, dev)
         if pages_out is None:
-            pages_out = self._new((d.batch, d.h_k, n_sel), i32, stream, zero=True)
+            pages_out = self._new((*self._count, n_sel), i32, stream, zero=True)
         else:
-            _need("pages_out", pages_out, i32, (d.batch, d.h_k, n_sel), dev)
+            _need("pages_out", pages_out, i32, (*self._count, n_sel), dev)
         if count_out is None:
-            count_out = self._new((d.batch, d.h_k), i32, stream)
+            count_out = self._new(self._count, i32, stream)
         else:
-            _need("count_out", count_out, i32, (d.batch, d.h_k), dev)
-        self._call(_lib.paged_select, d, n_sel, first, last, q, self.bounds, self.seq_lens, self.page_table,
+            _need("count_out", count_out, i32, self._count, dev)
+        self._call(_lib.paged_select, self.dims, n_sel, first, last, q, self.bounds, self.seq_lens, self.page_table,
                    pages_out, count_out, self.ws, stream=stream)
         return pages_out, count_out
 
     def decode(self, q, pages=None, count=None, out=None, stream=None):
         """Attention of one query token per sequence ([batch, h_q, d] bf16,
         rotated) over every cached position, or over select's pages; fp32."""
-        d, dev = self.dims, self.device
-        _need("q", q, torch.bfloat16, (d.batch, d.h_q, d.head_dim), dev)
+        dev = self.device
+        _need("q", q, torch.bfloat16, self._q, dev)
         if (pages is None) != (count is None):
             raise ValueError("pages and count go together")
         n_sel = 0
         if pages is not None:
             n_sel = pages.shape[-1]
-            _need("pages", pages, torch.int32, (d.batch, d.h_k, n_sel), dev)
-            _need("count", count, torch.int32, (d.batch, d.h_k), dev)
+            _need("pages", pages, torch.int32, (*self._count, n_sel), dev)
+            _need("count", count, torch.int32, self._count, dev)
         if out is None:
-            out = self._new((d.batch, d.h_q, self.dv), torch.float32, stream)
+            out = self._new(self._out, torch.float32, stream)
         else:
-            _need("out", out, torch.float32, (d.batch, d.h_q, self.dv), dev)
-        self._call(_lib.paged_decode, d, q, self.k_pages, self.v_pages, self.seq_lens, self.page_table, pages, count,
+            _need("out", out, torch.float32, self._out, dev)
+        self._call(_lib.paged_decode, self.dims, q, self.k_pages, self.v_pages, self.seq_lens, self.page_table, pages, count,
                    n_sel, out, self.ws, stream=stream)
         return out
 
