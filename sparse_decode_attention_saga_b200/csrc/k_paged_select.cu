@@ -12,15 +12,14 @@
 // its fragment is 16 contiguous bytes per lane).  A score is off by less than
 // E = 2^-14 max_h sum_d |q_d| max(|lo_d|, |hi_d|), which a third product gives
 // (at most 16 tile products of 17 addends, each cut at 2^-23 of the largest).
-// The row's last CTA finds the bin of the
-// n-th largest fp32 score in a histogram over equal steps between the row's
-// extremes (again between the bin's own while it is full), which leaves an
+// The row's last CTA finds the bin of the n-th largest fp32 score in a
+// histogram over equal steps between the row's extremes (again between the bin's own while it is full), which leaves an
 // interval [lo, hi] that the score lies in; pages 2E above it are in, pages 2E
 // below out, and only those between (a few, unless scores tie) are scored
 // again in 64 bits.  One launch.  Measured: batch 16 x 128K (64 rows of 2048 pages of
-// 64 positions, 34 MB of bounds) 17.5 us, of which the scores take 5.4 (6.3 TB/s)
+// 64 positions, 34 MB of bounds) 17.4 us, of which the scores take 5.4 (6.3 TB/s)
 // and the last CTAs' chain (ticket, extremes, histogram, cut, open pages, list) the
-// rest; one row of 2048 pages 12.8 us, the same chain.
+// rest; one row of 2048 pages 12.6 us, the same chain.
 #include <cuda_bf16.h>
 
 #include "paged.h"
@@ -82,18 +81,6 @@ __device__ __forceinline__ int block_prefix(int n, int& total, uint32_t (&buf)[2
     return before + incl - n;
 }
 
-// The largest of v over the block (min: negate).
-template <int kWarps>
-__device__ __forceinline__ float block_max(float v, uint32_t (&buf)[2][kWarps], int& turn) {
-    v = warp_max(v);
-    if ((threadIdx.x & 31) == 0) buf[turn][threadIdx.x >> 5] = __float_as_uint(v);
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) v = fmaxf(v, __uint_as_float(buf[turn][w]));
-    turn ^= 1;
-    return v;
-}
-
 template <int DK, int NT, int kThreads>
 __global__ void __launch_bounds__(kThreads, 512 / kThreads) select_kernel(const PagedSelectArgs a, const int groups) {
     constexpr int CH = DK / 32;  // 16-byte chunks of a bound row per lane
@@ -131,7 +118,12 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) select_kernel(const 
     const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + (static_cast<size_t>(b) * g.hq + kh * g.Gk) * DK;
     const __nv_bfloat16* boxes = reinterpret_cast<const __nv_bfloat16*>(a.bounds);
     float* scores = a.scores + static_cast<size_t>(row) * g.max_pages;
-    if (threadIdx.x == 0) n_band = 0;
+    // what the pick starts from, cleared while the first loads are on their way
+    const int n_words = (np + 31) / 32;
+    uint32_t* ranks = words + n_words;
+    for (int i = threadIdx.x; i < kBins; i += kThreads) bins[i] = 0u;
+    for (int i = threadIdx.x; i < n_words; i += kThreads) words[i] = 0u;
+    if (threadIdx.x == 0) n_band = 0, bin_lo = 0xffffffffu, bin_hi = 0u, the_bin = 0, the_rank = 1;
     // the queries' fragments, for hi, lo and the sum of magnitudes (k-steps of 16 dims: two to a lane's chunk)
     uint4 qraw[NT][CH];
 #pragma unroll
@@ -211,8 +203,6 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) select_kernel(const 
     if (threadIdx.x == 0) is_last = take_ticket(a.tickets + row) == static_cast<unsigned>(chunks - 1);
     __syncthreads();
     if (!is_last) return;
-    const int n_words = (np + 31) / 32;
-    uint32_t* ranks = words + n_words;
     auto forced = [&](int p) { return p < a.n_first || p >= np - a.n_last; };
     const int want = a.n_sel - a.n_first - a.n_last;  // pages to pick beside the forced ones
     // this thread's scores: every 512th page, 16 in registers (all there are, as a rule); no page: -inf
@@ -245,15 +235,22 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) select_kernel(const 
     each([&](float s, int) {
         if (s > -kInf) top = fmaxf(top, s), low = fmaxf(low, -s);
     });
-    top = block_max(top, sums, turn);
-    low = -block_max(low, sums, turn);
+    top = warp_max(top), low = warp_max(low);
+    if (lane == 0) sums[0][warp] = __float_as_uint(top), sums[1][warp] = __float_as_uint(low);
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+        top = fmaxf(top, __uint_as_float(sums[0][w])), low = fmaxf(low, __uint_as_float(sums[1][w]));
+    low = -low;
     // ---- the interval [lo, hi] of the want-th largest
     float lo = -kInf, hi = kInf;
     int rank = want;  // of it among the scores in (.., top]
     for (int level = 0; level < 4 && want > 0; ++level) {
-        for (int i = threadIdx.x; i < kBins; i += kThreads) bins[i] = 0u;
-        if (threadIdx.x == 0) bin_lo = 0xffffffffu, bin_hi = 0u, the_bin = 0, the_rank = 1;
-        __syncthreads();
+        if (level > 0) {
+            for (int i = threadIdx.x; i < kBins; i += kThreads) bins[i] = 0u;
+            if (threadIdx.x == 0) bin_lo = 0xffffffffu, bin_hi = 0u, the_bin = 0, the_rank = 1;
+            __syncthreads();
+        }
         const float step = top > low ? (kBins - 1) / (top - low) : 0.f;
         auto bin_of = [&](float s) { return static_cast<int>(fminf(fmaxf((s - low) * step, 0.f), kBins - 1.f)); };
         auto in = [&](float s) { return s >= lo && s <= hi; };  // of the level above's bin
@@ -295,7 +292,6 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) select_kernel(const 
     float cut_lo = lo - margin, cut_hi = hi + margin;
     if (want == 0) cut_lo = cut_hi = kInf;  // the forced pages only
     // ---- the pages above the cut and the forced ones, and those that the fp32 scores leave open
-    for (int i = threadIdx.x; i < n_words; i += kThreads) words[i] = 0u;
     __syncthreads();
     int above = 0;
     for (int r = 0; r < rounds; ++r) {
