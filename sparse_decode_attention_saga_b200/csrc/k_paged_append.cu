@@ -11,8 +11,8 @@
 //
 // Work unit: the new tokens of one page (the pages a sequence's run touches
 // are found from its length and the run's start alone), so that one CTA owns
-// a page's key bounds: no atomics on global memory, results do not depend on
-// the order of CTAs.  A row is handled by d/16 lanes, each with two 16-byte
+// a page's key bounds (each warp has its own, joined at the end): no atomics,
+// results do not depend on the order of CTAs.  A row is handled by d/16 lanes, each with two 16-byte
 // chunks that hold both halves of its pairs; a group of lanes keeps its
 // position's angles for all heads.
 //
@@ -21,8 +21,8 @@
 // bound leaves its bf16 rounding open (one value in some 2000); a quotient is
 // a product with the scale's reciprocal, put on a grid of 2^-12 (halves stay
 // halves, and no other quotient is within 2^-11 of one).  Measured, with the read
-// of the written rows: 20.7K tokens of 32/4/8 heads of 64 in 12 runs 66 us (248 MB,
-// 0.58 of the copy rate; 73 % of the issue slots), 256 single tokens 7.3 us.
+// of the written rows: 20.7K tokens of 32/4/8 heads of 64 in 12 runs 63.5 us (248 MB,
+// 0.60 of the copy rate; bound by issue), 256 single tokens 7.3 us.
 #include <cuda_bf16.h>
 
 #include "paged.h"
@@ -34,7 +34,7 @@ namespace {
 
 // Small CTAs, many to an SM: a unit's start is a chain of dependent loads (run,
 // length, page) that only other CTAs hide.
-constexpr int kThreads = 128;
+constexpr int kThreads = 128, kWarps = kThreads / 32;
 constexpr int kResident = 5;
 constexpr int kDepth = 4;        // rows of a lane in flight
 constexpr int kPartsPerSm = 12;  // CTAs per SM that a launch aims for by splitting the heads of its units
@@ -246,6 +246,20 @@ __device__ __forceinline__ uint32_t nibbles(const float (&y)[8], float s, float 
 __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); }
 __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
+// Eight bf16 values, each the smaller or larger of two.
+__device__ __forceinline__ uint4 least(uint4 x, uint4 y) {
+    auto f = [](uint32_t a, uint32_t b) { return as_u32(__hmin2(as_bf162(a), as_bf162(b))); };
+    return make_uint4(f(x.x, y.x), f(x.y, y.y), f(x.z, y.z), f(x.w, y.w));
+}
+__device__ __forceinline__ uint4 most(uint4 x, uint4 y) {
+    auto f = [](uint32_t a, uint32_t b) { return as_u32(__hmax2(as_bf162(a), as_bf162(b))); };
+    return make_uint4(f(x.x, y.x), f(x.y, y.y), f(x.z, y.z), f(x.w, y.w));
+}
+__device__ __forceinline__ uint4 shfl_xor4(uint4 v, int o) {
+    return make_uint4(__shfl_xor_sync(kFull, v.x, o), __shfl_xor_sync(kFull, v.y, o), __shfl_xor_sync(kFull, v.z, o),
+                      __shfl_xor_sync(kFull, v.w, o));
+}
+
 // The unit's rows of nk key heads from k0, nv value heads from v0 (rows of the
 // keys' width) and nq query heads from q0, one after another: keys and queries
 // rotated, keys and values rounded into the pages, queries to q_out.  A lane's
@@ -257,7 +271,7 @@ struct Heads {
 };
 template <int D, int MODE>
 __device__ __forceinline__ void write_rows(const PagedAppendArgs& a, const Unit& w, const Heads& n, bool value_rows,
-                                           uint32_t (*lo_hi)[2][D], uint4 (*slots)[2][kThreads]) {
+                                           uint4 (*lo_hi)[2][D / 8], uint4 (*slots)[2][kThreads]) {
     constexpr int LPR = D / 16;
     const PagedGeom& g = a.g;
     const Spread sp = spread<D>(w.rows);
@@ -321,45 +335,27 @@ __device__ __forceinline__ void write_rows(const PagedAppendArgs& a, const Unit&
             if (a.bounds && at < n.nk && w.rows == 1) {  // a single row: straight to the page's bounds
                 if (live && key) {
                     uint4* box = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.bounds) + (page_row * g.hk + n.k0 + i) * 2 * D);
-                    auto widen = [&](uint4* to, uint4 v, bool up) {
-                        if (w.old_rows) {
-                            const uint4 o = *to;
-                            const uint32_t x[4] = {v.x, v.y, v.z, v.w}, y[4] = {o.x, o.y, o.z, o.w};
-                            uint32_t r[4];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) r[j] = as_u32(up ? __hmax2(as_bf162(x[j]), as_bf162(y[j])) : __hmin2(as_bf162(x[j]), as_bf162(y[j])));
-                            v = make_uint4(r[0], r[1], r[2], r[3]);
-                        }
-                        *to = v;
-                    };
+                    auto widen = [&](uint4* to, uint4 v, bool up) { *to = w.old_rows ? up ? most(v, *to) : least(v, *to) : v; };
                     widen(box + pairs.ca, va, false);
                     widen(box + pairs.cb, vb, false);
                     widen(box + D / 8 + pairs.ca, va, true);
                     widen(box + D / 8 + pairs.cb, vb, true);
                 }
-            } else if (a.bounds && at < n.nk) {  // this warp's rows of each key head, then the CTA's
-                uint32_t lo[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w}, hi[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    hi[j] = row_live ? lo[j] : 0xff80ff80u;
-                    lo[j] = row_live ? lo[j] : 0x7f807f80u;
-                }
+            } else if (a.bounds && at < n.nk) {  // the warp's rows of each key head, into the warp's own boxes
+                const uint4 none_lo = make_uint4(0x7f807f80u, 0x7f807f80u, 0x7f807f80u, 0x7f807f80u);
+                const uint4 none_hi = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+                uint4 la = row_live ? va : none_lo, lb = row_live ? vb : none_lo, ha = row_live ? va : none_hi, hb = row_live ? vb : none_hi;
                 const int span = min(32, sp.rp * LPR);
-                for (int o = LPR; o < span; o <<= 1)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        lo[j] = as_u32(__hmin2(as_bf162(lo[j]), as_bf162(__shfl_xor_sync(kFull, lo[j], o))));
-                        hi[j] = as_u32(__hmax2(as_bf162(hi[j]), as_bf162(__shfl_xor_sync(kFull, hi[j], o))));
-                    }
+                for (int o = LPR; o < span; o <<= 1) {
+                    la = least(la, shfl_xor4(la, o)), lb = least(lb, shfl_xor4(lb, o));
+                    ha = most(ha, shfl_xor4(ha, o)), hb = most(hb, shfl_xor4(hb, o));
+                }
                 if (key && (threadIdx.x & 31) % span < LPR) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int d = 8 * (j < 4 ? pairs.ca : pairs.cb) + 2 * (j & 3);
-                        atomicMin(&lo_hi[i][0][d], float_to_key(bf16_lo(lo[j])));
-                        atomicMin(&lo_hi[i][0][d + 1], float_to_key(bf16_hi(lo[j])));
-                        atomicMax(&lo_hi[i][1][d], float_to_key(bf16_lo(hi[j])));
-                        atomicMax(&lo_hi[i][1][d + 1], float_to_key(bf16_hi(hi[j])));
-                    }
+                    uint4 (*box)[D / 8] = lo_hi[threadIdx.x / 32 * n.nk + i];
+                    box[0][pairs.ca] = least(la, box[0][pairs.ca]);
+                    box[0][pairs.cb] = least(lb, box[0][pairs.cb]);
+                    box[1][pairs.ca] = most(ha, box[1][pairs.ca]);
+                    box[1][pairs.cb] = most(hb, box[1][pairs.cb]);
                 }
             }
             issue(slot, at + kDepth * sp.hp);
@@ -373,7 +369,7 @@ __device__ __forceinline__ void write_rows(const PagedAppendArgs& a, const Unit&
 // Heads are numbered keys, values, queries; CTA y takes [y*per, (y+1)*per).
 template <int DK, int DV, int MODE>
 __global__ void __launch_bounds__(kThreads, kResident) append_kernel(const PagedAppendArgs a, int per) {
-    __shared__ uint32_t lo_hi[8][2][DK];
+    __shared__ uint4 lo_hi[kWarps * 8][2][DK / 8];  // a warp's bounds of each key head of the CTA's
     __shared__ uint4 slots[kDepth][2][kThreads];
     pdl_wait();  // lengths, tables and pages may be the previous kernels' results
     pdl_trigger();
@@ -389,8 +385,10 @@ __global__ void __launch_bounds__(kThreads, kResident) append_kernel(const Paged
         const int k1 = min(h1, g.hk);
         const bool bounds = a.bounds && h0 < k1 && w.rows > 1;
         if (bounds) {
-            for (int i = threadIdx.x; i < (k1 - h0) * 2 * DK; i += kThreads)
-                (&lo_hi[0][0][0])[i] = (i / DK) & 1 ? 0u : 0xffffffffu;
+            for (int i = threadIdx.x; i < kWarps * (k1 - h0) * 2 * (DK / 8); i += kThreads) {
+                const uint32_t none = i / (DK / 8) & 1 ? 0xff80ff80u : 0x7f807f80u;
+                (&lo_hi[0][0][0])[i] = make_uint4(none, none, none, none);
+            }
             __syncthreads();
         }
         const int v0 = max(h0 - g.hk, 0), v1 = min(h1 - g.hk, g.hv);
@@ -405,15 +403,17 @@ __global__ void __launch_bounds__(kThreads, kResident) append_kernel(const Paged
         if (!has_page(a, w) && threadIdx.x == 0) raise_device_error(a.err, kErrBounds);
         if (bounds && has_page(a, w)) {
             __syncthreads();
-            __nv_bfloat16* box = reinterpret_cast<__nv_bfloat16*>(a.bounds) +
-                                 (static_cast<size_t>(w.phys) * g.hk + h0) * 2 * DK;
-            for (int i = threadIdx.x; i < (k1 - h0) * 2 * DK; i += kThreads) {
-                float x = key_to_float((&lo_hi[0][0][0])[i]);
-                if (w.old_rows) {
-                    const float old = __bfloat162float(box[i]);
-                    x = (i / DK) & 1 ? fmaxf(x, old) : fminf(x, old);
-                }
-                box[i] = __float2bfloat16_rn(x);
+            uint4* box = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.bounds) +
+                                                  (static_cast<size_t>(w.phys) * g.hk + h0) * 2 * DK);
+            const int all = (k1 - h0) * 2 * (DK / 8);
+            for (int i = threadIdx.x; i < all; i += kThreads) {
+                const bool up = i / (DK / 8) & 1;
+                const uint4* own = &lo_hi[0][0][0] + i;
+                uint4 x = own[0];
+#pragma unroll
+                for (int k = 1; k < kWarps; ++k) x = up ? most(x, own[k * all]) : least(x, own[k * all]);
+                if (w.old_rows) x = up ? most(x, box[i]) : least(x, box[i]);
+                box[i] = x;
             }
         }
     }
