@@ -305,7 +305,8 @@ int saga_cache_append(const saga_dims* dims, const void* k_new, const void* v_ne
  * follow them.  Every one that is out of range (a negative length, a page
  * outside the pool, a list entry past the sequence) is skipped and sets the
  * sticky flag that saga_workspace_error reports as SAGA_ERR_BOUNDS.  Rows past
- * a sequence's end and pages outside its table hold anything.
+ * a sequence's end and pages outside its table hold anything.  New rows and
+ * queries are finite, after the rotation too.
  * Supported shapes: head_dim = v_head_dim in {64, 128}, or 32 with 64; h_k in
  * {1, 2, 4, 8}; h_v a multiple of h_k, h_q of h_v, h_q/h_k <= 16, h_q <= 128;
  * page_size in {16, 32, 64}; batch*h_q <= 65535; max_pages*page_size <= 2^30;

@@ -55,7 +55,6 @@ namespace saga {
 namespace {
 
 constexpr int kTile = 64;  // positions per tile
-constexpr int kMaxEntries = kTile / 16;
 constexpr int kMaxStages = 4;
 constexpr uint32_t kFull = 0xffffffffu;
 // Shared memory for a CTA's rings (227 KB at most; the static part is below 10 KB).
