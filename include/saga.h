@@ -359,10 +359,13 @@ size_t saga_paged_workspace_bytes(const saga_paged_dims* dims);
  *   bounds (nullable): the touched pages' key bounds, set anew where the call
  *   writes a page's first row, else widened.
  *   lens_out (nullable): the grown lengths; seq_lens itself, or apart from it.
- * A page that the call writes to belongs to one sequence only.  Rows past
- * max_pages * page_size or whose position is not in the rotation table are
- * not written (nor their queries) and set the sticky flag; so is the whole
- * page's part of the run where one of its positions is past the table.
+ * A page that the call writes to belongs to one sequence only; cu_new ascends.
+ * Rows past max_pages * page_size, of a page that is not in the pool or whose
+ * position is not in the rotation table are not written (nor their queries)
+ * and set the sticky flag; so is the whole page's part of the run where one of
+ * its positions is past the rotation table.  A sequence's length grows up to the first
+ * position that is not written (rows of the run behind it may be in their
+ * pages, but do not count).
  * q_out may be q_new itself (equal strides). */
 int saga_paged_append(const saga_paged_dims* dims, int32_t n_tokens, const int32_t* cu_new,
                       const int32_t* seq_lens, const int32_t* page_table, const void* k_new,

@@ -366,6 +366,53 @@ __device__ __forceinline__ void write_rows(const PagedAppendArgs& a, const Unit&
     cp_async_wait<0>();
 }
 
+// The grown lengths: each sequence's up to the first position that the call
+// does not write (none of a run or length out of range, none from a page on
+// that reaches past the rotation table or is not in the pool).  pages: whether
+// the runs' table entries have to be looked up for that.
+__device__ void write_lens(const PagedAppendArgs& a, bool pages) {
+    constexpr int kAhead = 4, kOwn = 16;  // entries on their way at once; pages that a lane looks up by itself
+    const PagedGeom& g = a.g;
+    const int lane = threadIdx.x & 31, shift = 31 - __clz(g.P), cap = g.max_pages * g.P;
+    // the first of pages p, p + step, .. up to p1 that is not in the pool, or p1 + 1
+    auto first_hole = [&](const int32_t* table, int p, int p1, int step) {
+        for (; p <= p1; p += kAhead * step) {
+            int e[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) e[k] = p + k * step <= p1 ? table[p + k * step] : 0;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (e[k] < 0 || e[k] >= g.n_pages) return p + k * step;
+        }
+        return p1 + 1;
+    };
+    for (int i0 = threadIdx.x - lane; i0 < g.b; i0 += kThreads) {
+        const int i = i0 + lane;
+        int len = 0, end = 0;
+        if (i < g.b) {
+            end = len = a.seq_lens[i];
+            const int t0 = a.cu ? a.cu[i] : 0, n = a.cu ? a.cu[i + 1] - t0 : 1;
+            if (t0 < 0 || n < 0 || t0 > a.n_tokens - n) {
+                raise_device_error(a.err, kErrBounds);
+            } else if (len >= 0 && len <= cap) {
+                end = min(len + n, cap);
+                if (a.rope && len + n > a.max_pos) end = max(len, min(end, a.max_pos >> shift << shift));
+            }
+        }
+        const int p0 = len >> shift, p1 = (end - 1) >> shift;
+        int hole = p1 + 1;
+        const bool any = pages && end > len, many = any && p1 - p0 >= kOwn;
+        if (any && !many) hole = first_hole(a.page_table + static_cast<size_t>(i) * g.max_pages, p0, p1, 1);
+        for (uint32_t left = __ballot_sync(kFull, many); left; left &= left - 1u) {  // long runs: by the whole warp
+            const int src = __ffs(left) - 1, q0 = __shfl_sync(kFull, p0, src), q1 = __shfl_sync(kFull, p1, src);
+            const int32_t* table = a.page_table + static_cast<size_t>(i0 + src) * g.max_pages;
+            const int h = __reduce_min_sync(kFull, first_hole(table, q0 + lane, q1, 32));
+            if (lane == src) hole = h;
+        }
+        if (i < g.b) a.lens_out[i] = hole > p1 ? end : max(len, hole << shift);
+    }
+}
+
 // Heads are numbered keys, values, queries; CTA y takes [y*per, (y+1)*per).
 template <int DK, int DV, int MODE>
 __global__ void __launch_bounds__(kThreads, kResident) append_kernel(const PagedAppendArgs a, int per) {
@@ -374,8 +421,13 @@ __global__ void __launch_bounds__(kThreads, kResident) append_kernel(const Paged
     pdl_wait();  // lengths, tables and pages may be the previous kernels' results
     pdl_trigger();
     const PagedGeom& g = a.g;
+    const bool lens_cta = a.lens_out && a.lens_out != a.seq_lens;  // the first column of CTAs has no unit
+    if (lens_cta && blockIdx.x == 0) {
+        if (blockIdx.y == 0) write_lens(a, true);
+        return;
+    }
     Unit w;
-    bool live = find_unit(a, blockIdx.x, w);
+    bool live = find_unit(a, blockIdx.x - lens_cta, w);
     if (live && a.rope && w.page * g.P + w.off + w.rows > a.max_pos) {  // positions past the table: not written
         if (threadIdx.x == 0) raise_device_error(a.err, kErrBounds);
         live = false;
@@ -400,7 +452,10 @@ __global__ void __launch_bounds__(kThreads, kResident) append_kernel(const Paged
             if (values.nv) write_rows<DV, kNoRotation>(a, w, values, true, nullptr, slots);
         }
         if (n.nk + n.nv + n.nq) write_rows<DK, MODE>(a, w, n, false, lo_hi, slots);
-        if (!has_page(a, w) && threadIdx.x == 0) raise_device_error(a.err, kErrBounds);
+        if (!has_page(a, w) && threadIdx.x == 0) {
+            raise_device_error(a.err, kErrBounds);
+            if (a.lens_out == a.seq_lens) atomicOr(a.ticket + 1, 1u);
+        }
         if (bounds && has_page(a, w)) {
             __syncthreads();
             uint4* box = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.bounds) +
@@ -417,25 +472,15 @@ __global__ void __launch_bounds__(kThreads, kResident) append_kernel(const Paged
             }
         }
     }
-    // The grown lengths: in place once every CTA has read the old ones, elsewhere at once.
-    if (a.lens_out) {
-        __shared__ bool mine;
-        const bool in_place = a.lens_out == a.seq_lens;
-        if (in_place) __syncthreads();
-        if (threadIdx.x == 0) {
-            mine = blockIdx.x == 0 && blockIdx.y == 0;
-            if (in_place) {
-                mine = atomicAdd(a.ticket, 1u) == gridDim.x * gridDim.y - 1;
-                if (mine) *a.ticket = 0u;
-            }
-        }
+    if (a.lens_out && !lens_cta) {  // in place: once every CTA has read the old lengths
+        __shared__ bool last;
         __syncthreads();
-        if (mine)
-            for (int i = threadIdx.x; i < g.b; i += kThreads) {
-                const int len = a.seq_lens[i], t0 = a.cu ? a.cu[i] : 0, n = a.cu ? a.cu[i + 1] - t0 : 1;
-                const bool run = t0 >= 0 && n >= 0 && t0 <= a.n_tokens - n && len >= 0;  // else skipped and flagged
-                a.lens_out[i] = run ? min(len + n, max(len, g.max_pages * g.P)) : len;
-            }
+        if (threadIdx.x == 0) last = take_ticket(a.ticket) == gridDim.x * gridDim.y - 1;
+        __syncthreads();
+        if (!last) return;
+        write_lens(a, __ldcg(a.ticket + 1) != 0u);
+        __syncthreads();
+        if (threadIdx.x < 2) a.ticket[threadIdx.x] = 0u;
     }
 }
 
@@ -493,7 +538,8 @@ cudaError_t launch(AppendKernel kern, const PagedAppendArgs& a, int heads, int s
     int parts = ((a.cu ? kPartsPerSm : 1) * sms + units - 1) / units;
     parts = parts < 1 ? 1 : parts > heads ? heads : parts;
     const int per = (heads + parts - 1) / parts;
-    const dim3 grid(units, (heads + per - 1) / per);
+    const int lens = a.lens_out && a.lens_out != a.seq_lens;  // a CTA of their own
+    const dim3 grid(units + lens, (heads + per - 1) / per);
     return launch_dependent(kern, grid, dim3(kThreads), 0, stream, a, per);
 }
 

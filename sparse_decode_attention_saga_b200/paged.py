@@ -129,7 +129,10 @@ class PagedCache:
         ends of the sequences: rows cu_new[b] .. cu_new[b+1]-1 are sequence b's
         (None: one row each).  Returns the rotated queries (None without
         q_new).  The grown lengths go to seq_lens, or to lens_out if given
-        (seq_lens then stays)."""
+        (seq_lens then stays); a sequence grows up to the first row that could
+        not be written (its page not in the pool, its position past the rotation
+        table: error() tells), and skipped rows' queries are left as they were
+        (without q_out: uninitialised)."""
         dev, bf, batch = self.device, torch.bfloat16, self._batch
         T = k_new.shape[0]
         _need("k_new", k_new, bf, (T, *self._k_row), dev, rows=True)
@@ -219,7 +222,9 @@ class PagedCache:
 
     def step(self, k_new, v_new, q_new, n_sel=None, first=1, last=1, out=None, stream=None):
         """One token of every sequence: its rows appended, its query attended
-        over the grown cache (over at most n_sel pages per key head if given)."""
+        over the grown cache (over at most n_sel pages per key head if given).
+        A sequence whose row could not be written (error() tells) keeps its
+        length, and its output row means nothing."""
         q = self.append(k_new, v_new, q_new, stream=stream)
         pages = count = None
         if n_sel is not None:
