@@ -39,6 +39,7 @@ constexpr int kResident = 5;
 constexpr int kDepth = 4;        // rows of a lane in flight
 constexpr int kPartsPerSm = 12;  // CTAs per SM that a launch aims for by splitting the heads of its units
 constexpr uint32_t kFull = 0xffffffffu;
+constexpr uint32_t kHole = 1u << 31;  // in the ticket: a page of the call's was missing
 // Where a work unit's tokens are: sequence, logical page, rows [first, first +
 // rows) of positions, and the index of the first one among the new tokens.
 struct Unit {
@@ -370,7 +371,7 @@ __device__ __forceinline__ void write_rows(const PagedAppendArgs& a, const Unit&
 // does not write (none of a run or length out of range, none from a page on
 // that reaches past the rotation table or is not in the pool).  pages: whether
 // the runs' table entries have to be looked up for that.
-__device__ void write_lens(const PagedAppendArgs& a, bool pages) {
+__device__ __forceinline__ void write_lens(const PagedAppendArgs& a, bool pages) {
     constexpr int kAhead = 4, kOwn = 16;  // entries on their way at once; pages that a lane looks up by itself
     const PagedGeom& g = a.g;
     const int lane = threadIdx.x & 31, shift = 31 - __clz(g.P), cap = g.max_pages * g.P;
@@ -399,9 +400,13 @@ __device__ void write_lens(const PagedAppendArgs& a, bool pages) {
                 if (a.rope && len + n > a.max_pos) end = max(len, min(end, a.max_pos >> shift << shift));
             }
         }
+        if (!pages) {
+            if (i < g.b) a.lens_out[i] = end;
+            continue;
+        }
         const int p0 = len >> shift, p1 = (end - 1) >> shift;
         int hole = p1 + 1;
-        const bool any = pages && end > len, many = any && p1 - p0 >= kOwn;
+        const bool any = end > len, many = any && p1 - p0 >= kOwn;
         if (any && !many) hole = first_hole(a.page_table + static_cast<size_t>(i) * g.max_pages, p0, p1, 1);
         for (uint32_t left = __ballot_sync(kFull, many); left; left &= left - 1u) {  // long runs: by the whole warp
             const int src = __ffs(left) - 1, q0 = __shfl_sync(kFull, p0, src), q1 = __shfl_sync(kFull, p1, src);
@@ -421,13 +426,12 @@ __global__ void __launch_bounds__(kThreads, kResident) append_kernel(const Paged
     pdl_wait();  // lengths, tables and pages may be the previous kernels' results
     pdl_trigger();
     const PagedGeom& g = a.g;
-    const bool lens_cta = a.lens_out && a.lens_out != a.seq_lens;  // the first column of CTAs has no unit
-    if (lens_cta && blockIdx.x == 0) {
+    if (blockIdx.x == a.lens_cta) {
         if (blockIdx.y == 0) write_lens(a, true);
         return;
     }
     Unit w;
-    bool live = find_unit(a, blockIdx.x - lens_cta, w);
+    bool live = find_unit(a, blockIdx.x, w);
     if (live && a.rope && w.page * g.P + w.off + w.rows > a.max_pos) {  // positions past the table: not written
         if (threadIdx.x == 0) raise_device_error(a.err, kErrBounds);
         live = false;
@@ -454,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, kResident) append_kernel(const Paged
         if (n.nk + n.nv + n.nq) write_rows<DK, MODE>(a, w, n, false, lo_hi, slots);
         if (!has_page(a, w) && threadIdx.x == 0) {
             raise_device_error(a.err, kErrBounds);
-            if (a.lens_out == a.seq_lens) atomicOr(a.ticket + 1, 1u);
+            if (a.lens_out == a.seq_lens) atomicOr(a.ticket, kHole);
         }
         if (bounds && has_page(a, w)) {
             __syncthreads();
@@ -472,15 +476,14 @@ __global__ void __launch_bounds__(kThreads, kResident) append_kernel(const Paged
             }
         }
     }
-    if (a.lens_out && !lens_cta) {  // in place: once every CTA has read the old lengths
-        __shared__ bool last;
+    if (a.lens_out == a.seq_lens) {  // grown in place: once every CTA has read the old lengths
+        __shared__ uint32_t before;
         __syncthreads();
-        if (threadIdx.x == 0) last = take_ticket(a.ticket) == gridDim.x * gridDim.y - 1;
+        if (threadIdx.x == 0) before = atomicAdd(a.ticket, 1u);
         __syncthreads();
-        if (!last) return;
-        write_lens(a, __ldcg(a.ticket + 1) != 0u);
-        __syncthreads();
-        if (threadIdx.x < 2) a.ticket[threadIdx.x] = 0u;
+        if ((before & ~kHole) != gridDim.x * gridDim.y - 1) return;
+        if (threadIdx.x == 0) *a.ticket = 0u;
+        write_lens(a, before & kHole);
     }
 }
 
@@ -530,7 +533,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const PagedAppendArgs a,
 
 using AppendKernel = void (*)(const PagedAppendArgs, int);
 
-cudaError_t launch(AppendKernel kern, const PagedAppendArgs& a, int heads, int sms, cudaStream_t stream) {
+cudaError_t launch(AppendKernel kern, PagedAppendArgs a, int heads, int sms, cudaStream_t stream) {
     const PagedGeom& g = a.g;
     const int units = a.cu ? a.n_tokens / g.P + 2 * g.b : g.b;
     // two waves of CTAs even the ends out: 20.7K tokens in 12 runs 68.8 us at 5 CTAs an SM, 65.6 at 8, 63.5 at 12,
@@ -538,8 +541,9 @@ cudaError_t launch(AppendKernel kern, const PagedAppendArgs& a, int heads, int s
     int parts = ((a.cu ? kPartsPerSm : 1) * sms + units - 1) / units;
     parts = parts < 1 ? 1 : parts > heads ? heads : parts;
     const int per = (heads + parts - 1) / parts;
-    const int lens = a.lens_out && a.lens_out != a.seq_lens;  // a CTA of their own
-    const dim3 grid(units + lens, (heads + per - 1) / per);
+    const bool apart = a.lens_out && a.lens_out != a.seq_lens;
+    a.lens_cta = apart ? units : ~0u;
+    const dim3 grid(units + apart, (heads + per - 1) / per);
     return launch_dependent(kern, grid, dim3(kThreads), 0, stream, a, per);
 }
 

@@ -30,7 +30,7 @@ SAGA_HD constexpr int paged_block_bytes(int P, int d) { return P * (d / 2 + 2); 
 // Offsets up to `scores` depend on the batch, the heads and their dims only;
 // the tickets are zero on entry and left at zero.
 struct PagedWsLayout {
-    size_t err;      // uint32 sticky flag; words 2, 3: the append's ticket, and whether a page was missing (256-byte header)
+    size_t err;      // uint32 sticky flag; word 2: the append's ticket (256-byte header)
     size_t tickets;  // uint32 [b*hv]
     size_t records;  // float  [kPagedMaxCtas][2][columns of a work row * (2 + dv)]
     size_t firsts;   // float  [kPagedMaxCtas][kPagedWarps][columns of a work row * (2 + dv)]
@@ -95,7 +95,8 @@ struct PagedAppendArgs {
     void* q_out;       // [n_tokens][hq][dk]
     void *k_out, *v_out;  // read: [n_tokens][hk][dk], [n_tokens][hv][dv]
     int32_t* lens_out;  // nullable; may be seq_lens
-    uint32_t* ticket;   // [2], zero on entry and exit
+    uint32_t* ticket;  // zero on entry and exit
+    uint32_t lens_cta;  // column of CTAs that writes lengths apart from seq_lens (~0: none; set by the launch)
     uint32_t* err;
 };
 cudaError_t launch_paged_append(const PagedAppendArgs& a, int sms, cudaStream_t stream);
