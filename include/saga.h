@@ -406,7 +406,12 @@ int saga_paged_select(const saga_paged_dims* dims, int32_t n_sel, int32_t n_firs
  * sel_pages[b, kh(i), 0 .. sel_cnt[b, kh(i)] - 1] (each listed once, in any
  * order).  out [batch, h_q, v_head_dim] fp32; rows of zeros where there is no
  * position.  The numbers are multiplied as they are (exact in fp16), scales are
- * applied to logits and probabilities in fp32. */
+ * applied to logits and probabilities in fp32; of a probability times its
+ * value row's scale the sums take 22 bits, none below 2^-31 of the largest such
+ * product of the query head.  That holds for queries below 2^100 in magnitude,
+ * for value rows whose scale is 0 or from 2^-45 to 2^56 (smaller ones keep fewer
+ * bits, next to larger ones the least weights are lost), and for logits below
+ * 2^25 in magnitude. */
 int saga_paged_decode(const saga_paged_dims* dims, const void* q, const void* k_pages,
                       const void* v_pages, const int32_t* seq_lens, const int32_t* page_table,
                       const int32_t* sel_pages, const int32_t* sel_cnt, int32_t n_sel, float* out,

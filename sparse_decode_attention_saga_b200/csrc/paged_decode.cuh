@@ -11,10 +11,11 @@
 // u = n + 8 as a subnormal, u 2^-24, its -8 sum(q) put into the accumulator's
 // start; values: 1024 + u less 1032), a query is shifted by a power of two
 // per head into fp16's range (its 8 bits stay whole), and a probability times
-// its row's scale goes in as two fp16 halves (22 bits), relative to the
-// largest scale met so far.  The row scale of the keys multiplies the logit.
-// A new reference for the exponentials is taken only when a product nears
-// fp16's end.  The contraction's order is free, so the nibbles of a word pair
+// its row's scale goes in as two fp16 halves (22 bits, none below 2^-31 of the
+// largest such product of its query head so far: neither a row of little weight
+// nor another head takes bits away).  The row scale of the keys multiplies the logit.
+// A new reference for the exponentials (a whole number: rescaling and merging
+// are exact) is taken only when a product nears fp16's end.  The contraction's order is free, so the nibbles of a word pair
 // up as they lie (dims of the keys, queries laid out alike), and the values,
 // which need pairs of positions, are transposed byte-wise on the way out of
 // shared memory.
@@ -63,14 +64,14 @@ constexpr int kRingBytes = 216 * 1024;
 // (batch 1 at 8K: 14.9 us at 16, 14.2 at 8, 14.8 at 4).
 constexpr int kMinTiles = 8;
 constexpr int kRound = 4;  // tiles between two arrivals at the pace barrier
-// A probability times its row's scale stands in fp16 in units of 2^-kUnit of the
-// largest scale: room for a logit to pass the accumulators' reference before a
-// new one is taken, when a product reaches 2^15.
+// A probability times its row's scale is 2^6 to 2^kUnit where it sets its
+// column's reference: room for others to pass it before a new one is taken,
+// when a product reaches 2^15.
 constexpr int kUnit = 8;
-// Biased exponent that the largest scale is taken for at least (2^-67): exponentials
-// in that unit and their sums stay far from fp32's end.
-constexpr int kLeastExpo = 60;
-// The reference before a row's first position: its product overflows and brings one.
+// Biased exponent that a scale is taken for at least (2^-45) where a reference is
+// set: exponentials (2^53 then) and their sums stay far from fp32's end, rows of zeros among them.
+constexpr int kLeastExpo = 82;
+// The reference before a row's first position: its exponential overflows and brings one.
 constexpr float kNone = -1e30f;
 // log2(e) / sqrt(d): logits count in powers of two
 template <int D>
@@ -365,10 +366,9 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
     };
 
     // ---- consumer state
-    int row = -1, seen = 0, expo = 0;  // seen: flags of the row's tiles so far; expo: biased exponent of the largest scale
+    int row = -1, seen = 0;  // seen: flags of the row's tiles so far
     uint32_t qf[NT][KS][2];
-    float c0[NT][2], colf[NT][2], m[NT][2], l[NT][2];
-    float base[NT][2];  // the reference less the unit: exponentials are in units of 2^-kUnit of the largest scale
+    float c0[NT][2], colf[NT][2], m[NT][2], l[NT][2];  // m: the reference of the exponentials
     float acc[ACC][MT][4];
     // Rows gq and gq + 8 of a key tile are positions 2 gq and 2 gq + 1 (of 16): after the transposition a lane
     // then has the probabilities of positions 4 tq, 4 tq + 2 and 4 tq + 1, 4 tq + 3, as it has the values.
@@ -384,7 +384,6 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
     auto begin_row = [&](int r) {
         row = r;
         seen = 0;
-        expo = kLeastExpo;
         const int vg = r % nvg, bk = r / nvg;  // bk = b * hk + kh
         const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) +
                                  (static_cast<size_t>(bk) * g.nvk + vg * NVU) * g.Gv * DK;
@@ -434,7 +433,6 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
                 c0[nt][i] = __shfl_sync(kFull, start, (2 * tq + i) * 4);
                 colf[nt][i] = __shfl_sync(kFull, f, (2 * tq + i) * 4);
                 m[nt][i] = kNone;
-                base[nt][i] = kNone;
                 l[nt][i] = 0.f;
             }
         }
@@ -488,13 +486,12 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) l[nt][i] += __shfl_xor_sync(kFull, l[nt][i], o);
-        const float scale_unit = pow2i(expo - 127 - kUnit);
         float f[NT][2];
         const bool whole = seen == 3;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) f[nt][i] = !whole ? scale_unit : l[nt][i] > 0.f ? __fdividef(1.f, l[nt][i]) : 0.f;
+            for (int i = 0; i < 2; ++i) f[nt][i] = !whole ? 1.f : l[nt][i] > 0.f ? __fdividef(1.f, l[nt][i]) : 0.f;
         // an end of the range stays in this warp's ring (its copies are all in), an earlier piece goes to the workspace
         float* dst = end_of_range ? reinterpret_cast<float*>(my_ring)
                                   : a.firsts + (static_cast<size_t>(blockIdx.x) * kWarps + warp) * kRecord;
@@ -504,7 +501,7 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     if (8 * nt + 2 * tq + i < kColumns)
-                        reinterpret_cast<float2*>(dst)[8 * nt + 2 * tq + i] = make_float2(m[nt][i], l[nt][i] * scale_unit);
+                        reinterpret_cast<float2*>(dst)[8 * nt + 2 * tq + i] = make_float2(m[nt][i], l[nt][i]);
         }
         float* to = row_out(row) + lane_dim(lane);
         float fx[ACC][2];
@@ -601,54 +598,50 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) x[nt][2 * r + i] = __fmaf_rn(x[nt][2 * r + i], s, off[r]);
             }
-        // p = 2^(logit - reference + unit), y = p times its row's scale, in two fp16 halves
-        float p[NT][4], y[NT][4];
+        // p = 2^(logit - reference), y = p times its row's scale, in two fp16 halves, sum = l and the p of its column
+        float p[NT][4], y[NT][4], sum[NT][2];
         uint32_t hi[NT][2], lo[NT][2];
         auto products = [&]() {
             __half2 top = bits_half2(0u);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const float s = r ? bf16_hi(vscale[nt]) : bf16_lo(vscale[nt]);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        p[nt][2 * r + i] = exp2_approx(__fmaf_rn(x[nt][2 * r + i], colf[nt][i], -base[nt][i]));
+                        p[nt][2 * r + i] = exp2_approx(__fmaf_rn(x[nt][2 * r + i], colf[nt][i], -m[nt][i]));
                         y[nt][2 * r + i] = p[nt][2 * r + i] * s;
                     }
                     const __half2 h = __floats2half2_rn(y[nt][2 * r], y[nt][2 * r + 1]);
                     hi[nt][r] = half2_bits(h);
                     top = __hmax2_nan(top, h);
                 }
-            return ((half2_bits(top) + 0x08000800u) & 0x80008000u) != 0u;  // a half at 2^15 or above, or no number
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    sum[nt][i] = l[nt][i] + p[nt][i] + p[nt][2 + i];
+                }
+            }
+            // a half at 2^15 or above, or no number
+            return ((half2_bits(top) + 0x08000800u) & 0x80008000u) != 0u;
         };
-        if (__any_sync(kFull, products())) {  // a new reference: the largest logit and scale so far
-            uint32_t top = 0;
+        if (__any_sync(kFull, products())) {  // a new reference: the largest product so far is below 2^kUnit of it
             float f[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                top = max(top, max(vscale[nt] & 0x7fffu, (vscale[nt] >> 16) & 0x7fffu));
+                const float e0 = static_cast<float>(max((vscale[nt] >> 7) & 0xffu, static_cast<uint32_t>(kLeastExpo)));
+                const float e1 = static_cast<float>(max((vscale[nt] >> 23) & 0xffu, static_cast<uint32_t>(kLeastExpo)));
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    float v = fmaxf(x[nt][i], x[nt][2 + i]);
+                    float v = fmaxf(__fmaf_rn(x[nt][i], colf[nt][i], e0), __fmaf_rn(x[nt][2 + i], colf[nt][i], e1));
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
-                    v = fmaxf(v * colf[nt][i], m[nt][i]);
+                    v = fmaxf(ceilf(v) - static_cast<float>(kUnit + 126), m[nt][i]);
                     f[nt][i] = exp2_approx(m[nt][i] - v);
                     m[nt][i] = v;
-                }
-            }
-            const int en = max(expo, static_cast<int>(__reduce_max_sync(kFull, top) >> 7));
-            const float shift = en - expo < 126 ? pow2i(expo - en) : 0.f;
-            expo = en;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    base[nt][i] = m[nt][i] - static_cast<float>(kUnit + 127 - en);
-                    f[nt][i] *= shift;
                     l[nt][i] = f[nt][i] > 0.f ? l[nt][i] * f[nt][i] : 0.f;
                 }
+            }
 #pragma unroll
             for (int xx = 0; xx < ACC; ++xx) {
                 float fx[2];
@@ -664,8 +657,7 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                l[nt][0] += p[nt][2 * r];
-                l[nt][1] += p[nt][2 * r + 1];
+                l[nt][r] = sum[nt][r];
                 const float2 back = __half22float2(bits_half2(hi[nt][r]));
                 lo[nt][r] = half2_bits(__floats2half2_rn(y[nt][2 * r] - back.x, y[nt][2 * r + 1] - back.y));
             }

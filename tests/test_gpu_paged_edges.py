@@ -87,3 +87,99 @@ def test_lengths_stop_at_the_end_of_the_rotation_table(in_place):
     got = grown_by(p, news, in_place, k, v, q)
     assert p.cache.error() == _lib.SAGA_ERR_BOUNDS
     assert got == [32, 40, 36, 41, 40, 40, 40]
+
+
+# ---------------------------------------------------------------- magnitudes far apart
+
+def weighted(p, q, lists=None):
+    """(out, bound) in 64 bits; the bound goes by the rows' weights, not by the largest value.
+
+    With w = softmax and e the relative error of a weight (a logit's dk + 2 roundings of 2^-24 of its terms'
+    magnitudes, 2^-20 for the exponential and the two halves of a product, 2^-16 for sums of a few hundred
+    steps), numerator and denominator are off by e sum w |v| each.  A product w s of weight and row scale is
+    held to 2^-25 of the column's own unit, in which the largest product is at least 2^6, and multiplies
+    numbers up to 7: N 7 2^-31 max(w s)."""
+    hq, hk, hv, dk, dv = p.layout
+    s, P = p.state, p.P
+    qn = f64(q)
+    out, bound = np.zeros((len(s["seq_lens"]), hq, dv)), np.zeros((len(s["seq_lens"]), hq, dv))
+    for b, n in enumerate(s["seq_lens"]):
+        if not n:
+            continue
+        for i in range(hq):
+            k = ref.rows(s["k_pages"], P, dk, s["page_table"][b], i * hk // hq, int(n))
+            v = ref.rows(s["v_pages"], P, dv, s["page_table"][b], i * hv // hq, int(n))
+            x = k @ qn[b, i] / np.sqrt(dk)
+            w = np.exp(x - x.max())
+            w /= w.sum()
+            out[b, i] = w @ v
+            e = (dk + 2) * 2.0 ** -24 * (np.abs(k) @ np.abs(qn[b, i])).max() / np.sqrt(dk) + 2.0 ** -20 + 2.0 ** -16
+            bound[b, i] = 2 * e * (w @ np.abs(v)) + n * 7 * 2.0 ** -31 * (w * np.abs(v).max(1) / 7).max()
+    return out, bound
+
+
+def set_scales(p, name, b, head, scales):
+    """The first len(scales) row scales of a head of sequence b (bf16 values)."""
+    d, P, s = p.layout[3 if name == "k_pages" else 4], p.P, p.state
+    raw = torch.from_numpy(np.ascontiguousarray(scales)).bfloat16().view(torch.uint8).numpy().reshape(-1, 2)
+    for i, r in enumerate(raw):
+        at = P * d // 2 + 2 * (i % P)
+        s[name][s["page_table"][b, i // P], head, at:at + 2] = r
+
+
+def set_rows(p, name, b, head, numbers):
+    """The first rows of a head of sequence b: every number of row i is numbers[i]."""
+    d, P, s = p.layout[3 if name == "k_pages" else 4], p.P, p.state
+    for i, n in enumerate(numbers):
+        u = int(n) + 8
+        s[name][s["page_table"][b, i // P], head, i % P * d // 2:(i % P + 1) * d // 2] = u | u << 4
+
+
+def push(p):
+    p.cache.k_pages.copy_(torch.from_numpy(p.state["k_pages"]))
+    p.cache.v_pages.copy_(torch.from_numpy(p.state["v_pages"]))
+
+
+def check_weighted(p, q):
+    want, bound = weighted(p, q)
+    got = f64(p.cache.decode(q.cuda()))
+    assert p.cache.error() == _lib.SAGA_OK
+    worst = np.abs(got - want) / np.maximum(bound, 1e-300)
+    assert worst.max() <= 1, "%.3g times the bound at %s" % (worst.max(), np.unravel_index(worst.argmax(), worst.shape))
+
+
+# value heads per key head in one work row: 2, 4 and 2 of at most four, eight and four query heads
+SHARED = [((32, 4, 8, 64, 64), 64), ((16, 1, 8, 64, 64), 16), ((32, 2, 4, 64, 64), 32), ((12, 1, 2, 128, 128), 16),
+          ((16, 2, 8, 32, 64), 64)]
+
+
+@pytest.mark.parametrize("layout,P", SHARED)
+def test_value_heads_of_scales_far_apart(layout, P):
+    """Value heads of one key head at scales 1, 2^-24, 2^-36 and 2^20 of each other: each is as exact as alone."""
+    lens = [3000, 65, 700]
+    p = filled(layout, P, lens, 41)
+    hv = layout[2]
+    for b, n in enumerate(lens):
+        for h in range(hv):
+            set_scales(p, "v_pages", b, h, ref.bf16(np.full(n, 0.3) * (1 + np.arange(n) % 5 / 8) *
+                                                    2.0 ** (0, -24, -36, 20)[(h + b) % 4]))
+    push(p)
+    check_weighted(p, p.query())
+
+
+@pytest.mark.parametrize("layout,P", SHARED + [((16, 1, 1, 128, 128), 64), ((4, 1, 2, 64, 64), 16)])
+@pytest.mark.parametrize("up", [10, 20, 30])
+def test_a_large_row_without_weight(layout, P, up):
+    """Rows at the starts whose value scale is 2^up above the others' and whose weight is next to nothing
+    do not take bits from the rows that carry it."""
+    lens = [1500, 40, 9000]
+    p = filled(layout, P, lens, 42)
+    hq, hk, hv, dk, dv = layout
+    for b, n in enumerate(lens):
+        for h in range(hk):  # the first rows: logits far below all others
+            set_rows(p, "k_pages", b, h, [-7] * 3)
+            set_scales(p, "k_pages", b, h, np.full(3, 8.0))
+        for h in range(hv):
+            set_scales(p, "v_pages", b, h, np.full(3, 2.0 ** up))
+    push(p)
+    check_weighted(p, (0.1 + 0.4 * torch.rand(len(lens), hq, dk, generator=p.gen)).bfloat16())
