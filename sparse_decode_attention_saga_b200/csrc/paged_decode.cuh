@@ -15,7 +15,8 @@
 // largest such product of its query head so far: neither a row of little weight
 // nor another head takes bits away).  The row scale of the keys multiplies the logit.
 // A new reference for the exponentials (a whole number: rescaling and merging
-// are exact) is taken only when a product nears fp16's end.  The contraction's order is free, so the nibbles of a word pair
+// are exact) is taken only when a product nears fp16's end or the sum of the
+// exponentials fp32's.  The contraction's order is free, so the nibbles of a word pair
 // up as they lie (dims of the keys, queries laid out alike), and the values,
 // which need pairs of positions, are transposed byte-wise on the way out of
 // shared memory.
@@ -71,6 +72,9 @@ constexpr int kUnit = 8;
 // Biased exponent that a scale is taken for at least (2^-45) where a reference is
 // set: exponentials (2^53 then) and their sums stay far from fp32's end, rows of zeros among them.
 constexpr int kLeastExpo = 82;
+// A new reference where a lane's sums of exponentials reach this (by rows whose
+// scale is too small for their products to ask for one).
+constexpr float kMostSum = 1.2676506e30f;  // 2^100
 // The reference before a row's first position: its exponential overflows and brings one.
 constexpr float kNone = -1e30f;
 // log2(e) / sqrt(d): logits count in powers of two
@@ -603,6 +607,7 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
         uint32_t hi[NT][2], lo[NT][2];
         auto products = [&]() {
             __half2 top = bits_half2(0u);
+            float all = 0.f;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -620,10 +625,11 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     sum[nt][i] = l[nt][i] + p[nt][i] + p[nt][2 + i];
+                    all += sum[nt][i];
                 }
             }
-            // a half at 2^15 or above, or no number
-            return ((half2_bits(top) + 0x08000800u) & 0x80008000u) != 0u;
+            // a half at 2^15 or above, sums far up, or no number
+            return ((half2_bits(top) + 0x08000800u) & 0x80008000u) != 0u || !(all < kMostSum);
         };
         if (__any_sync(kFull, products())) {  // a new reference: the largest product so far is below 2^kUnit of it
             float f[NT][2];

@@ -183,3 +183,22 @@ def test_a_large_row_without_weight(layout, P, up):
             set_scales(p, "v_pages", b, h, np.full(3, 2.0 ** up))
     push(p)
     check_weighted(p, (0.1 + 0.4 * torch.rand(len(lens), hq, dk, generator=p.gen)).bfloat16())
+
+
+@pytest.mark.parametrize("layout", [(32, 4, 8, 64, 64), (16, 1, 1, 128, 128), (32, 2, 4, 64, 64), (16, 2, 8, 32, 64)])
+@pytest.mark.parametrize("gap", [110.0, 119.3, 119.6, 130.0])
+def test_zero_value_rows_far_above_the_first(layout, gap):
+    """Rows of zeros whose weight is 2^gap times the ones' before them, then rows like those and as heavy:
+    the zeros' weight counts, and nothing overflows."""
+    hq, hk, hv, dk, dv = layout
+    n = 96
+    p = filled(layout, 32, [n], 44)
+    pos = np.arange(n)
+    scale = ref.bf16(gap * np.log(2) * np.sqrt(dk) / (7 * dk))  # logits of 7 dk scale / sqrt(dk) with queries of 1
+    for h in range(hk):
+        set_rows(p, "k_pages", 0, h, [7] * n)
+        set_scales(p, "k_pages", 0, h, np.where(pos < 16, 0.0, scale))
+    for h in range(hv):
+        set_scales(p, "v_pages", 0, h, np.where((pos >= 16) & (pos < 64), 0.0, 1.0))
+    push(p)
+    check_weighted(p, torch.ones(1, hq, dk).bfloat16())
