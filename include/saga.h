@@ -411,7 +411,7 @@ int saga_paged_select(const saga_paged_dims* dims, int32_t n_sel, int32_t n_firs
  * product of the query head.  That holds for queries below 2^100 in magnitude,
  * for value rows whose scale is 0 or from 2^-45 to 2^56 (smaller ones keep fewer
  * bits, next to larger ones the least weights are lost), and for logits below
- * 2^25 in magnitude. */
+ * 2^25 in magnitude: a head whose largest logit is not gets NaN. */
 int saga_paged_decode(const saga_paged_dims* dims, const void* q, const void* k_pages,
                       const void* v_pages, const int32_t* seq_lens, const int32_t* page_table,
                       const int32_t* sel_pages, const int32_t* sel_cnt, int32_t n_sel, float* out,

@@ -75,8 +75,10 @@ constexpr int kLeastExpo = 82;
 // A new reference where a lane's sums of exponentials reach this (by rows whose
 // scale is too small for their products to ask for one).
 constexpr float kMostSum = 1.2676506e30f;  // 2^100
+// A reference from this on is no number: fp32 would leave the unit out of it.
+constexpr float kMostLogit = 67108864.f;  // 2^26, logits in powers of two
 // The reference before a row's first position: its exponential overflows and brings one.
-constexpr float kNone = -1e30f;
+constexpr float kNone = -3e38f;
 // log2(e) / sqrt(d): logits count in powers of two
 template <int D>
 constexpr float kLogitScaleOf = D == 32 ? 0.25503486f : D == 64 ? 0.18033688f : 0.12751743f;
@@ -643,6 +645,7 @@ __global__ void __launch_bounds__((Shape<DK, DV, CW, NVU>::W * 32), 1)
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
                     v = fmaxf(ceilf(v) - static_cast<float>(kUnit + 126), m[nt][i]);
+                    if (fabsf(v) >= kMostLogit && v != kNone) v = __uint_as_float(0x7fffffffu);
                     f[nt][i] = exp2_approx(m[nt][i] - v);
                     m[nt][i] = v;
                     l[nt][i] = f[nt][i] > 0.f ? l[nt][i] * f[nt][i] : 0.f;

@@ -186,6 +186,34 @@ def test_a_large_row_without_weight(layout, P, up):
 
 
 @pytest.mark.parametrize("layout", [(32, 4, 8, 64, 64), (16, 1, 1, 128, 128), (32, 2, 4, 64, 64), (16, 2, 8, 32, 64)])
+@pytest.mark.parametrize("up,sign", [(53, -7), (53, 7), (-34, -7), (-34, 7), (-40, -7)])
+def test_logits_of_every_magnitude(layout, up, sign):
+    """One row's logit far from the others, all of them large: it takes all, whatever their sign.  Where
+    fp32's steps are larger than the unit (2^53: logits of 1e31, apart by 2^80 steps) the result is NaN."""
+    hq, hk, hv, dk, dv = layout
+    lens = [200, 17, 64]
+    p = filled(layout, 32, lens, 43)
+    best = [133, 4, 63]
+    for b, n in enumerate(lens):
+        pos = np.arange(n)
+        near, far = (2.0 ** 50, 2.0 ** 51 * (1 + pos % 7 / 8)) if sign < 0 else (2.0 ** 52, 2.0 ** 50 * (1 + pos % 7 / 8))
+        for h in range(hk):
+            set_rows(p, "k_pages", b, h, [sign] * n)
+            set_scales(p, "k_pages", b, h, np.where(pos == best[b], near, far))
+    push(p)
+    q = torch.full((3, hq, dk), 2.0 ** up).bfloat16()
+    got = f64(p.cache.decode(q.cuda()))
+    assert p.cache.error() == _lib.SAGA_OK
+    for b, n in enumerate(lens):
+        for i in range(hq):
+            v = ref.rows(p.state["v_pages"], 32, dv, p.state["page_table"][b], i * hv // hq, n)[best[b]]
+            if up > 0:
+                assert np.isnan(got[b, i]).all()
+            else:
+                assert np.all(np.abs(got[b, i] - v) <= 2.0 ** -20 * np.abs(v) + 2.0 ** -31 * np.abs(v).max())
+
+
+@pytest.mark.parametrize("layout", [(32, 4, 8, 64, 64), (16, 1, 1, 128, 128), (32, 2, 4, 64, 64), (16, 2, 8, 32, 64)])
 @pytest.mark.parametrize("gap", [110.0, 119.3, 119.6, 130.0])
 def test_zero_value_rows_far_above_the_first(layout, gap):
     """Rows of zeros whose weight is 2^gap times the ones' before them, then rows like those and as heavy:
