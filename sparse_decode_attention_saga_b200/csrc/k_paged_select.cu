@@ -33,6 +33,8 @@ constexpr int kPer = 16;     // pages a thread holds in registers
 constexpr int kBand = 1024;  // pages scored again in shared memory
 constexpr int kBins = 2048;
 constexpr int kFewInBin = 24;  // pages in the threshold's bin that need no finer histogram
+constexpr float kLeast = 1e-34f;  // above what products and sums below fp32's normal range are off by in a score
+constexpr float kMost = 1e33f;    // margins below: scores (2^14 of it) and their sums are finite
 constexpr uint32_t kFull = 0xffffffffu;
 
 __device__ __forceinline__ unsigned long long double_to_key(double x) {
@@ -229,8 +231,8 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) select_kernel(const 
     };
     int turn = 0;
     load(0);
-    // 2E: 2^-14 of the row's largest size, itself within 2^-14
-    const float margin = 2.f * 6.2e-5f * __uint_as_float(__ldcg(a.row_max + row));
+    // 2E: 2^-14 of the row's largest size, itself within 2^-14, and what fp32's subnormals may lose
+    const float margin = 2.f * 6.2e-5f * __uint_as_float(__ldcg(a.row_max + row)) + kLeast;
     float top = -kInf, low = -kInf;
     each([&](float s, int) {
         if (s > -kInf) top = fmaxf(top, s), low = fmaxf(low, -s);
@@ -290,7 +292,9 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) select_kernel(const 
         __syncthreads();  // the bins are cleared next
     }
     float cut_lo = lo - margin, cut_hi = hi + margin;
-    if (want == 0) cut_lo = cut_hi = kInf;  // the forced pages only
+    if (!(margin < kMost)) cut_lo = -kInf, cut_hi = kInf;  // scores past fp32's end: every page is open
+    if (want == 0) cut_lo = cut_hi = kInf;                 // the forced pages only
+    auto is_open = [&](float s) { return !(s < cut_lo) && !(s > cut_hi); };  // (a score that is no number too)
     // ---- the pages above the cut and the forced ones, and those that the fp32 scores leave open
     __syncthreads();
     int above = 0;
@@ -305,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) select_kernel(const 
             const uint32_t bits = __ballot_sync(kFull, must || over);
             if (lane == 0 && p < np) words[p / 32] = bits;
             above += over;
-            if (p < np && !must && !over && x[j] >= cut_lo) {
+            if (p < np && !must && is_open(x[j])) {
                 const int at = atomicAdd(&n_band, 1);
                 if (at < kBand) band_page[at] = p, band_key[at] = 0ull;
             }
@@ -323,13 +327,13 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) select_kernel(const 
 #pragma unroll
         for (int i = lane; i < DK; i += 32) {
             const float v = __bfloat162float(q[h * DK + i]);
-            s += static_cast<double>(fmaxf(v * __bfloat162float(box[i]), v * __bfloat162float(box[DK + i])));
+            s += static_cast<double>(v) * __bfloat162float(box[v > 0.f ? DK + i : i]);  // exact: 16 bits
         }
         return s;
     };
     if (open == take) {
         each([&](float s, int p) {
-            if (s >= cut_lo && s <= cut_hi) set(p);
+            if (is_open(s)) set(p);
         });
     } else if (open <= kBand) {
         // a page and head per warp, four at a time (their loads and sums overlap)
@@ -362,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) select_kernel(const 
         for (int p = warp; p < np; p += kWarps) {
             const float s = __ldcg(scores + p);
             unsigned long long k = 0ull;
-            if (!forced(p) && s >= cut_lo && s <= cut_hi)
+            if (!forced(p) && is_open(s))
                 for (int h = 0; h < g.Gk; ++h) {
                     double v = partial(p, h);
 #pragma unroll

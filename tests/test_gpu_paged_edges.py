@@ -230,3 +230,22 @@ def test_zero_value_rows_far_above_the_first(layout, gap):
         set_scales(p, "v_pages", 0, h, np.where((pos >= 16) & (pos < 64), 0.0, 1.0))
     push(p)
     check_weighted(p, torch.ones(1, hq, dk).bfloat16())
+
+
+# ---------------------------------------------------------------- selection
+
+@pytest.mark.parametrize("layout", [(4, 1, 2, 64, 64), (12, 1, 2, 128, 128), (16, 2, 8, 32, 64), (16, 1, 1, 64, 64)])
+@pytest.mark.parametrize("qs,ks", [(1e-30, 1e-12), (1e-30, 1e-14), (1e-38, 1e-10), (1e-39, 1.0), (1e-39, 2.0 ** 60),
+                                   (1e-20, 1e-20), (1.0, 1e-39), (2.0 ** 55, 2.0 ** 55), (2.0 ** 70, 2.0 ** 60), (1e35, 1e36)])
+def test_select_scores_of_every_magnitude(layout, qs, ks):
+    """Scores at and below fp32's smallest numbers and past its largest, subnormal queries and keys."""
+    lens = [16 * 300 + 5, 16 * 90, 16 * 4]
+    p = filled(layout, 16, lens, 45)
+    box = ref.bf16(p.state["bounds"] * ks)
+    p.cache.bounds.copy_(torch.from_numpy(box))
+    q = (p.query().float() * qs).bfloat16()
+    for n_sel, first, last in ((7, 0, 0), (40, 1, 2)):
+        want = ref.select(f64(q), box, lens, p.state["page_table"], 16, n_sel, first, last)
+        pages, count = p.cache.select(q.cuda(), n_sel, first, last)
+        got = [[pages[b, h, :count[b, h]].tolist() for h in range(layout[1])] for b in range(len(lens))]
+        assert got == want
