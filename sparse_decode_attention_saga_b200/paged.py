@@ -112,16 +112,36 @@ class PagedCache:
             fn(*args, self._on(stream))
 
     def grow_table(self, lens) -> None:
-        """Hands pool pages to sequences in order, enough for lens[b] positions
-        of sequence b each (host numbers); the whole table is written."""
+        """Hands pool pages to sequences, enough for lens[b] positions of
+        sequence b each (host numbers).  Pages that hold cached positions (the
+        first seq_lens[b] of each sequence) stay with it; all others are dealt
+        out in order, and the whole table is written.  Waits for the device."""
         d = self.dims
         need = [-(-int(n) // d.page_size) for n in lens]
-        if len(need) != d.batch or any(n < 0 for n in lens) or max(need) > d.max_pages or sum(need) > d.n_pages:
+        if len(need) != d.batch or any(n < 0 for n in lens):
+            raise ValueError("the pool or the table does not hold these lengths (one of each sequence, 0 or more)")
+        cached, table = self.seq_lens.tolist(), self.page_table.cpu()
+        rows = torch.full((d.batch, d.max_pages), -1, dtype=torch.int32)
+        held = set()
+        for b, n in enumerate(cached):
+            if not 0 <= n <= d.max_pages * d.page_size:
+                raise ValueError(f"sequence {b}'s cached length is {n}")
+            n = -(-n // d.page_size)
+            own = table[b, :n].tolist()
+            if any(not 0 <= p < d.n_pages for p in own):
+                raise ValueError(f"the table does not hold the cached pages of sequence {b}")
+            rows[b, :n] = table[b, :n]
+            need[b] = max(need[b], n)
+            held.update(own)
+            cached[b] = n
+        free = [p for p in range(d.n_pages) if p not in held]
+        if max(need) > d.max_pages or sum(need) - sum(cached) > len(free):
             raise ValueError("the pool or the table does not hold these lengths")
-        rows, at = torch.full((d.batch, d.max_pages), -1, dtype=torch.int32), 0
+        at = 0
         for b, n in enumerate(need):
-            rows[b, :n] = torch.arange(at, at + n, dtype=torch.int32)
-            at += n
+            more = n - cached[b]
+            rows[b, cached[b]:n] = torch.tensor(free[at:at + more], dtype=torch.int32)
+            at += more
         self.page_table.copy_(rows)
 
     def append(self, k_new, v_new, q_new=None, cu_new=None, q_out=None, lens_out=None, stream=None):

@@ -202,3 +202,40 @@ def test_reference_holds_rows_within_half_a_step():
         got = ref.row(block, 16, 64, 3 + i)
         assert np.abs(got - x[i]).max() <= scale * (0.5 + 7 * 2.0 ** -8)
     assert paged.block_bytes(64, 128) == 64 * 66
+
+
+def test_grow_table_keeps_the_pages_of_cached_rows():
+    c = cache()
+    c.grow_table([64, 64])
+    c.seq_lens.copy_(torch.tensor([64, 1], dtype=torch.int32))
+    c.grow_table([129, 128])
+    assert c.page_table[0, :4].tolist() == [0, 2, 3, -1] and c.page_table[1, :3].tolist() == [1, 4, -1]
+    c.seq_lens.copy_(torch.tensor([65, 1], dtype=torch.int32))
+    c.grow_table([640, 0])  # a sequence keeps what its rows are in; pages without rows are dealt out anew
+    assert c.page_table[0].tolist() == [0, 2] + list(range(3, 11)) and c.page_table[1].tolist() == [1] + [-1] * 9
+    before = c.page_table.clone()
+    for bad in ([641, 1], [640], [-1, 1]):
+        with pytest.raises(ValueError):
+            c.grow_table(bad)
+    c.seq_lens[1] = 65  # more rows than the table has pages of
+    with pytest.raises(ValueError, match="cached pages of sequence 1"):
+        c.grow_table([640, 65])
+    c.seq_lens[1] = 641
+    with pytest.raises(ValueError, match="cached length"):
+        c.grow_table([640, 65])
+    assert torch.equal(c.page_table, before)
+    c.seq_lens.zero_()  # all over: dealt out anew
+    c.grow_table([65, 64])
+    assert c.page_table[:, :3].tolist() == [[0, 1, -1], [2, -1, -1]]
+
+
+def test_grow_table_with_shared_and_few_pages():
+    """Sequences that share their first page (a common prefix); a pool that is just large enough."""
+    c = PagedCache(3, 4, 1, 2, 64, 5, 4, page_size=16, device="cpu")
+    c.page_table[0, :2] = torch.tensor([4, 1])
+    c.page_table[1, 0] = c.page_table[2, 0] = 4
+    c.seq_lens.copy_(torch.tensor([20, 16, 9], dtype=torch.int32))
+    c.grow_table([32, 48, 20])
+    assert c.page_table.tolist() == [[4, 1, -1, -1], [4, 0, 2, -1], [4, 3, -1, -1]]
+    with pytest.raises(ValueError, match="hold these"):
+        c.grow_table([33, 48, 20])
