@@ -38,6 +38,8 @@ def _need(name, t, dtype, shape, device, rows=False):
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the cache on {device}")
     step, head, one = t.stride() if t.dim() == 3 else (0, 0, 0)
+    if shape[1:2] == (1,):  # a single head's stride means nothing
+        head = shape[2]
     if not rows or one != 1 or head != shape[2] or step < shape[1] * shape[2] or step % 8:
         raise ValueError(f"{name} must be contiguous" + (" in each row, rows a multiple of 8 elements apart"
                                                          if rows else ""))

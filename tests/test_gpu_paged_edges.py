@@ -249,3 +249,17 @@ def test_select_scores_of_every_magnitude(layout, qs, ks):
         pages, count = p.cache.select(q.cuda(), n_sel, first, last)
         got = [[pages[b, h, :count[b, h]].tolist() for h in range(layout[1])] for b in range(len(lens))]
         assert got == want
+
+
+# ---------------------------------------------------------------- rows as they come
+
+def test_append_rows_of_one_head_out_of_a_wider_matrix():
+    p = Pair((4, 1, 2, 64, 64), 16, [60, 60], [9, 0], 50)
+    k, v, q = p.rows(30)
+    wide = torch.zeros(30, 200, dtype=torch.bfloat16, device="cuda")
+    wide[:, :64] = k[:, 0].cuda()
+    cu = np.array([0, 17, 30], np.int32)
+    want = ref.append(p.state, f64(k), f64(v), f64(q), cu, p.table.numpy(), p.rot, False)
+    got = p.cache.append(wide[:, None, :64], v.cuda(), q.cuda(), cu_new=torch.from_numpy(cu).cuda())
+    assert np.array_equal(f64(got), want)
+    p.check_pool()

@@ -239,3 +239,16 @@ def test_grow_table_with_shared_and_few_pages():
     assert c.page_table.tolist() == [[4, 1, -1, -1], [4, 0, 2, -1], [4, 3, -1, -1]]
     with pytest.raises(ValueError, match="hold these"):
         c.grow_table([33, 48, 20])
+
+
+def test_rows_of_one_head_may_have_any_head_stride():
+    """x[:, None, :d] of a wider matrix: the head dim of size 1 has an arbitrary stride."""
+    bf = torch.bfloat16
+    wide = torch.zeros(5, 200, dtype=bf)
+    paged._need("k_new", wide[:, None, :64], bf, (5, 1, 64), wide.device, rows=True)
+    odd = wide.as_strided((5, 1, 64), (200, 3, 1))
+    paged._need("k_new", odd, bf, (5, 1, 64), wide.device, rows=True)
+    for bad in (wide.as_strided((5, 1, 64), (200, 3, 2)), wide.as_strided((5, 1, 64), (36, 3, 1)),
+                wide.as_strided((5, 1, 64), (100, 3, 1)), wide.as_strided((5, 2, 64), (200, 65, 1))):
+        with pytest.raises(ValueError, match="k_new"):
+            paged._need("k_new", bad, bf, tuple(bad.shape), wide.device, rows=True)
