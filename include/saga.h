@@ -306,7 +306,8 @@ int saga_cache_append(const saga_dims* dims, const void* k_new, const void* v_ne
  * outside the pool, a list entry past the sequence) is skipped and sets the
  * sticky flag that saga_workspace_error reports as SAGA_ERR_BOUNDS.  Rows past
  * a sequence's end and pages outside its table hold anything.  New rows and
- * queries are finite, after the rotation too.
+ * queries are finite, after the rotation too (others make the rows they are in
+ * NaN, and what attends to those).
  * Supported shapes: head_dim = v_head_dim in {64, 128}, or 32 with 64; h_k in
  * {1, 2, 4, 8}; h_v a multiple of h_k, h_q of h_v, h_q/h_k <= 16, h_q <= 128;
  * page_size in {16, 32, 64}; batch*h_q <= 65535; max_pages*page_size <= 2^30;
@@ -350,7 +351,8 @@ size_t saga_paged_workspace_bytes(const saga_paged_dims* dims);
  * positions seq_lens[b] ...  Keys (and queries) are rotated first (rope null:
  * not); each row of a head is then held as
  *   scale = bf16(max|x| / 7), n = clamp(round-half-even(x / scale), -7, 7)
- * (n = 0 where the scale is 0).
+ * (n = 0 where the scale is 0); a row with a number that is not finite gets a
+ * scale of NaN and reads as NaN.
  *   k_new [n_tokens, h_k, head_dim], v_new [n_tokens, h_v, v_head_dim], q_new
  *   [n_tokens, h_q, head_dim] bf16, rows k_stride, v_stride, q_stride elements
  *   apart (multiples of 8; slices of a fused projection's output will do).

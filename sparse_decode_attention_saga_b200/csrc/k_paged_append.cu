@@ -247,6 +247,9 @@ __device__ __forceinline__ uint32_t nibbles(const float (&y)[8], float s, float 
 __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); }
 __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
+// The larger magnitudes of two pairs of bf16 values, as bits.
+__device__ __forceinline__ uint32_t magnitudes(uint32_t x, uint32_t y) { return __vmaxu2(x & 0x7fff7fffu, y & 0x7fff7fffu); }
+
 // Eight bf16 values, each the smaller or larger of two.
 __device__ __forceinline__ uint4 least(uint4 x, uint4 y) {
     auto f = [](uint32_t a, uint32_t b) { return as_u32(__hmin2(as_bf162(a), as_bf162(b))); };
@@ -314,15 +317,18 @@ __device__ __forceinline__ void write_rows(const PagedAppendArgs& a, const Unit&
                 to[pairs.cb] = vb;
             }
             if (at < n.nk + n.nv) {  // rounding: keys or values among the CTA's heads of this time
-                float ya[8], yb[8], m = 0.f;
+                float ya[8], yb[8];
                 unpack8(va, ya);
                 unpack8(vb, yb);
+                // the largest magnitude, by its bits: what is not finite is above all that is
+                uint32_t most2 = __vmaxu2(__vmaxu2(magnitudes(va.x, va.y), magnitudes(va.z, va.w)),
+                                          __vmaxu2(magnitudes(vb.x, vb.y), magnitudes(vb.z, vb.w)));
 #pragma unroll
-                for (int j = 0; j < 8; ++j) m = fmaxf(m, fmaxf(fabsf(ya[j]), fabsf(yb[j])));
-#pragma unroll
-                for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+                for (int o = LPR / 2; o > 0; o >>= 1) most2 = __vmaxu2(most2, __shfl_xor_sync(kFull, most2, o));
+                const uint32_t top = max(most2 & 0xffffu, most2 >> 16);
+                const float m = __uint_as_float(top << 16);
                 // (a seventh of 8 bits is at least a fourteenth of a step from every middle: the product rounds like the quotient)
-                const __nv_bfloat16 scale = __float2bfloat16_rn(m * 0.142857149f);
+                const __nv_bfloat16 scale = __float2bfloat16_rn(top < 0x7f80u ? m * 0.142857149f : __uint_as_float(0x7fffffffu));
                 const float s = __bfloat162float(scale), inv = __fdividef(1.f, s);
                 const uint32_t wa = nibbles(ya, s, inv), wb = nibbles(yb, s, inv);
                 if (live && (key || value)) {

@@ -263,3 +263,32 @@ def test_append_rows_of_one_head_out_of_a_wider_matrix():
     got = p.cache.append(wide[:, None, :64], v.cuda(), q.cuda(), cu_new=torch.from_numpy(cu).cuda())
     assert np.array_equal(f64(got), want)
     p.check_pool()
+
+
+# ---------------------------------------------------------------- rows that are not finite
+
+@pytest.mark.parametrize("layout", [(4, 1, 2, 64, 64), (12, 1, 2, 128, 128), (16, 2, 8, 32, 64)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_rows_that_are_not_finite_stay_so(layout, bad):
+    """A row with one number that is not finite reads back as NaN and makes a decode over it NaN; the rows
+    beside it are whole."""
+    hq, hk, hv, dk, dv = layout
+    p = Pair(layout, 16, [80], [5], 48, rot=0)
+    k, v, q = p.rows(40)
+    k[7, 0, dk - 1] = bad
+    v[21, hv - 1, 3] = bad
+    p.cache.append(k.cuda(), v.cuda(), cu_new=torch.tensor([0, 40], dtype=torch.int32, device="cuda"))
+    got_k, got_v = p.cache.read(40, torch.tensor([0, 40], dtype=torch.int32, device="cuda"), torch.tensor([5], dtype=torch.int32, device="cuda"))
+    k[7, 0], v[21, hv - 1] = 0, 0
+    ref.append(p.state, f64(k), f64(v), None, np.array([0, 40]), None, 0, False)
+    s = p.state
+    for out, name, heads, d, at in ((got_k, "k_pages", hk, dk, (7, 0)), (got_v, "v_pages", hv, dv, (21, hv - 1))):
+        want = np.stack([ref.rows(s[name], 16, d, s["page_table"][0], h, 45)[5:] for h in range(heads)], 1)
+        got = f64(out)
+        assert np.isnan(got[at]).all()
+        got[at] = 0
+        assert np.array_equal(got, ref.bf16(want))
+    out = f64(p.cache.decode(q[:1].cuda()))[0]
+    G = hq // hv
+    assert np.isnan(out[:hq // hk]).all()             # key head 0's query heads
+    assert np.isnan(out[(hv - 1) * G:]).all()         # the last value head's
