@@ -292,3 +292,49 @@ def test_rows_that_are_not_finite_stay_so(layout, bad):
     G = hq // hv
     assert np.isnan(out[:hq // hk]).all()             # key head 0's query heads
     assert np.isnan(out[(hv - 1) * G:]).all()         # the last value head's
+
+
+# ---------------------------------------------------------------- many sequences
+
+@pytest.mark.parametrize("layout,P,batch", [((32, 4, 8, 64, 64), 64, 60), ((8, 2, 2, 64, 64), 16, 1100), ((16, 2, 8, 32, 64), 32, 100),
+                                            ((12, 1, 2, 128, 128), 16, 170), ((16, 1, 1, 64, 64), 16, 200),
+                                            ((16, 1, 1, 128, 128), 32, 160), ((32, 2, 2, 32, 64), 16, 90)])
+def test_select_more_rows_than_sms(layout, P, batch):
+    """More rows than SMs (the smaller CTAs), most of a few pages, one beyond 4096 of them."""
+    rng = np.random.default_rng(5)
+    lens = [int(n) for n in rng.integers(0, 60 * P, batch)]
+    lens[3], lens[batch // 2], lens[-1] = 4200 * P + 1, 700 * P, 0
+    p = filled(layout, P, lens, 46)
+    q = p.query()
+    for n_sel, first, last in ((1, 0, 0), (25, 1, 2)):
+        want = ref.select(f64(q), p.state["bounds"], lens, p.state["page_table"], P, n_sel, first, last)
+        pages, count = p.cache.select(q.cuda(), n_sel, first, last)
+        assert p.cache.error() == _lib.SAGA_OK
+        pages, count = pages.tolist(), count.tolist()
+        assert [[r[:n] for r, n in zip(*rn)] for rn in zip(pages, count)] == want
+
+
+@pytest.mark.parametrize("P", [16, 64])
+@pytest.mark.parametrize("batch", [32, 33, 64, 65, 1024, 1025, 1100])
+def test_runs_of_many_sequences(batch, P):
+    """Ragged runs over more sequences than a warp's search takes in one step, empty ones at its steps' borders;
+    the rows read back by the same runs."""
+    layout = (2, 1, 1, 64, 64)
+    rng = np.random.default_rng(batch)
+    news = rng.integers(0, 3, batch)
+    for step in (31, 32, 33, 34, 63, 64, 65, 66, 1023, 1024, 1056):
+        if step < batch:
+            news[step] = step % 2 * 40
+    news[0], news[-1] = 70, 5
+    lens = rng.integers(0, 40, batch)
+    p = Pair(layout, P, (lens + news).tolist(), lens.tolist(), 47)
+    got = p.append(news.tolist())
+    assert got.shape[0] == news.sum()
+    p.check_pool()
+    cu = torch.tensor(np.concatenate(([0], np.cumsum(news))), dtype=torch.int32, device="cuda")
+    k, v = p.cache.read(int(news.sum()), cu, torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    s = p.state
+    for out, name in ((k, "k_pages"), (v, "v_pages")):
+        want = np.concatenate([ref.rows(s[name], P, 64, s["page_table"][b], 0, int(lens[b] + news[b]))[lens[b]:]
+                               for b in range(batch)])
+        assert np.array_equal(f64(out)[:, 0], ref.bf16(want))
