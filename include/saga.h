@@ -329,7 +329,7 @@ typedef struct {
 /* Position rotation: pair (x1, x2) of a row at position p becomes
  * (x1 c - x2 s, x2 c + x1 s) with c = table[p][i], s = table[p][rot_dim/2 + i]
  * for pair i < rot_dim/2, computed exactly to one fp32 rounding and stored as
- * bf16.  Pair i is dims (i, i + rot_dim/2), or (2i, 2i+1) with interleaved;
+ * bf16 (to one step of bf16 where a product is below 2^-110).  Pair i is dims (i, i + rot_dim/2), or (2i, 2i+1) with interleaved;
  * dims from rot_dim on stay as they are.  rot_dim: a multiple of 16, at most
  * head_dim. */
 typedef struct {
@@ -391,7 +391,8 @@ int saga_paged_read(const saga_paged_dims* dims, int32_t n_tokens, const int32_t
  * <= n_sel), the rest by descending score, of equal ones the lower index:
  *   score(page) = max over the key head's query heads of
  *                 sum_d max(q_d * bounds[page,0,d], q_d * bounds[page,1,d]),
- * compared in 64 bits: no key of the page has a larger q.k.
+ * compared in 64 bits: no key of the page, as it was before rounding to 4 bits,
+ * has a larger q.k (a rounded one may, by half a step).
  *   q [batch, h_q, head_dim] bf16 (rotated)
  *   sel_pages [batch, h_k, n_sel] int32: page indices in the sequence,
  *   ascending; entries past sel_cnt are left as they were.

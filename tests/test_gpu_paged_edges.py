@@ -338,3 +338,27 @@ def test_runs_of_many_sequences(batch, P):
         want = np.concatenate([ref.rows(s[name], P, 64, s["page_table"][b], 0, int(lens[b] + news[b]))[lens[b]:]
                                for b in range(batch)])
         assert np.array_equal(f64(out)[:, 0], ref.bf16(want))
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("mag,steps", [(1e30, 0), (1.0, 0), (1e-31, 0), (1e-36, 1), (1e-39, 1)])
+def test_rotation_of_every_magnitude(inter, mag, steps):
+    """Rotated rows bit for bit while a pair's products are above 2^-110, else to one step of bf16."""
+    T, d = 3000, 128
+    p = Pair((12, 1, 2, d, d), 64, [T], [0], 49, interleaved=inter)
+    k, v, q = p.rows(T)
+    # magnitudes within 2^-4 of each other: no pair's products are far below mag
+    q = (torch.where(q < 0, -1.0, 1.0) * (1 + q.float().abs().clamp(max=3)) * mag).bfloat16()
+    got = p.cache.append(k.cuda(), v.cuda(), q.cuda(), cu_new=torch.tensor([0, T], dtype=torch.int32, device="cuda")).cpu()
+    c, s = p.table[:T, None, :d // 2].double(), p.table[:T, None, d // 2:].double()
+    x = q.double()
+    a, b = (x[..., 0::2], x[..., 1::2]) if inter else (x[..., :d // 2], x[..., d // 2:])
+    y = torch.stack((a * c - b * s, b * c + a * s), -1).flatten(-2) if inter else torch.cat((a * c - b * s, b * c + a * s), -1)
+    want = y.float().bfloat16()
+    if steps == 0:
+        small = torch.stack((torch.minimum((a * c).abs(), (b * s).abs()), torch.minimum((b * c).abs(), (a * s).abs())), -1) < 2.0 ** -110
+        small = small.flatten(-2) if inter else torch.cat((small[..., 0], small[..., 1]), -1)
+        assert small.float().mean() < 0.2
+        assert torch.equal(got[~small], want[~small])
+    one = torch.maximum(want.abs().double() * 2.0 ** -7, torch.tensor(2.0 ** -133, dtype=torch.float64))
+    assert ((got.double() - want.double()).abs() <= one).all()
