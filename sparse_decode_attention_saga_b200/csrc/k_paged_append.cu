@@ -20,9 +20,12 @@
 // is two operations and an error bound, recomputed exactly only where the
 // bound leaves its bf16 rounding open (one value in some 2000); a quotient is
 // a product with the scale's reciprocal, put on a grid of 2^-12 (halves stay
-// halves, and no other quotient is within 2^-11 of one).  Measured, with the read
-// of the written rows: 20.7K tokens of 32/4/8 heads of 64 in 12 runs 63.5 us (248 MB,
-// 0.60 of the copy rate; bound by issue), 256 single tokens 7.3 us.
+// halves, and no other quotient is within 2^-11 of one).  Measured on the device
+// (graph replays): 20.7K tokens of 32/4/8 heads of 64 in 12 runs 50.6 us and their
+// rows read back 12.7 (together 248 MB, 0.60 of the copy rate; the append is bound
+// by issue); 256 single tokens 4.6 us, with the lengths grown in place 5.6 us (a
+// ticket and the last CTA's pass over the lengths), from Python without a graph
+// 11.2 us: the host's share.
 #include <cuda_bf16.h>
 
 #include "paged.h"
@@ -159,7 +162,7 @@ struct Pairs {
             s[4 * h] = y.x, s[4 * h + 1] = y.y, s[4 * h + 2] = y.z, s[4 * h + 3] = y.w;
         }
     }
-    // The rotated chunks.  All lanes of the warp take part.
+    // The rotated chunks.
     __device__ __forceinline__ void turn(uint4& ra, uint4& rb) const {
         if (MODE == kNoRotation) return;
         float xa[8], xb[8];

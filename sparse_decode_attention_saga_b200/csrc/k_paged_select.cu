@@ -1,9 +1,11 @@
 // Page selection of the sparse decode: the pages of each (sequence, key head)
 // whose keys can reach the largest logits.
 //
-// A page's key bounds lo, hi (per dim the smallest and largest key) bound the
-// logit of every key in it: q.k <= sum_d max(q_d lo_d, q_d hi_d) = q+ . hi +
-// q- . lo, with q+ = max(q, 0) and q- = min(q, 0).  The score of a page is the
+// A page's key bounds lo, hi (per dim the smallest and largest key, as they were
+// before rounding to 4 bits) bound the logit of each of those keys: q.k <=
+// sum_d max(q_d lo_d, q_d hi_d) = q+ . hi + q- . lo, with q+ = max(q, 0) and
+// q- = min(q, 0) (a published way to rank pages).  The rounded keys, which the
+// decode reads, may pass it by half a step.  The score of a page is the
 // largest such bound over the key head's query heads, compared in 64 bits (the
 // lower index first where equal).
 //
@@ -16,10 +18,11 @@
 // histogram over equal steps between the row's extremes (again between the bin's own while it is full), which leaves an
 // interval [lo, hi] that the score lies in; pages 2E above it are in, pages 2E
 // below out, and only those between (a few, unless scores tie) are scored
-// again in 64 bits.  One launch.  Measured: batch 16 x 128K (64 rows of 2048 pages of
-// 64 positions, 34 MB of bounds) 17.4 us, of which the scores take 5.4 (6.3 TB/s)
-// and the last CTAs' chain (ticket, extremes, histogram, cut, open pages, list) the
-// rest; one row of 2048 pages 12.6 us, the same chain.
+// again in 64 bits, as are all where fp32 does not hold the scores.  One launch.
+// Measured: batch 16 x 128K (64 rows of 2048 pages of 64 positions, 34 MB of
+// bounds) 17.7 us, of which the scores take 5.4 (6.3 TB/s) and the last CTAs' chain
+// (ticket, extremes, histogram, cut, open pages, list) the rest; one row of 2048
+// pages 12.6 us, the same chain.
 #include <cuda_bf16.h>
 
 #include "paged.h"
@@ -207,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) select_kernel(const 
     if (!is_last) return;
     auto forced = [&](int p) { return p < a.n_first || p >= np - a.n_last; };
     const int want = a.n_sel - a.n_first - a.n_last;  // pages to pick beside the forced ones
-    // this thread's scores: every 512th page, 16 in registers (all there are, as a rule); no page: -inf
+    // this thread's scores: every kThreads-th page, 16 in registers (all there are, as a rule); no page: -inf
     const int rounds = (np + kRound - 1) / kRound;
     float x[kPer];
     auto load = [&](int round) {

@@ -35,13 +35,18 @@
 // SM's older warps ran first and left the younger ones to finish alone, at
 // half the issue rate (batch 16 x 128K: CTAs ended at 150 and at 215 us).
 //
-// Measured (32/4/8 heads of 64, batch 16 x 128K, 856 MB): 173 us, 4.9 TB/s, 0.75
-// of the copy rate, at 1965 MHz; 196 us when repeated until the power cap holds
-// the clock at 1750 MHz.  Bound by issue: 848 warp instructions a tile (379 of
-// them on the half-rate integer pipe, unpacking nibbles), 61 % of the issue
-// slots with the four warps a scheduler that the registers allow; tensor pipe
-// 21 %, DRAM reads 1.00 times the cache.  Batch 1 at 8K: 14 us, the chain of
-// lengths, table, copies, one tile, two merges.
+// Measured (32/4/8 heads of 64, batch 16 x 128K, 856 MB): 174 us, 4.9 TB/s, 0.75
+// of the copy rate, at 1965 MHz; 195 us when repeated until the power cap holds
+// the clock at 1750 MHz (time goes by the clock).  864 warp instructions a tile
+// (384 on the half-rate integer pipe, unpacking nibbles): 56 % of the issue
+// slots, 50 % of that pipe, tensor pipe 21 %, DRAM reads 1.00 times the cache.
+// None is full: what is left is latency with the four warps a scheduler that the
+// registers allow (of the 7.4 cycles from one issue of a warp to the next, 1.6
+// wait for a result of fixed latency, 1.1 for another warp's turn, 1.0 for a
+// pipe, 0.7 at barriers, 0.6 for memory).
+// Batch 1 at 8K: 14.1 us, the chain of lengths, table, copies, one tile, two
+// merges; most of it waits at barriers (8.6 of 20) for warps that fetch the body's
+// instructions for the first time (4.4).
 #pragma once
 
 #include <cuda_bf16.h>
